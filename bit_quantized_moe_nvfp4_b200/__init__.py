@@ -27,9 +27,15 @@ __all__ = [
     "moe_nvfp4_ep_reduce", "EP_MAX_PARTS", "moe_nvfp4_router", "moe_nvfp4_forward_logits",
     "moe_nvfp4_shared_expert", "moe_nvfp4_layer", "moe_nvfp4_layer_workspace_size",
     "nvfp4_w4a4_prepare_scales", "moe_nvfp4_forward_w4a4", "moe_nvfp4_w4a4_workspace_size",
+    "moe_nvfp4_pre_norm", "moe_nvfp4_pre_norm_int8", "moe_nvfp4_pre_norm_backward",
+    "moe_nvfp4_post_norm", "moe_nvfp4_post_norm_backward",
+    "moe_nvfp4_norm_backward_workspace_size", "ACT_SILU", "ACT_GELU", "moe_nvfp4_gate_up",
+    "moe_nvfp4_gate_up_backward", "moe_nvfp4_gate_up_backward_workspace_size",
+    "nvfp4_int8_quantize", "nvfp4_int8_matmul",
 ]
 
 PATH_AUTO, PATH_GEMV, PATH_GEMM = 0, 1, 2
+ACT_SILU, ACT_GELU = 0, 1    # gate activations of moe_nvfp4_gate_up
 WORKSPACE_ZERO_BYTES = 512   # head of a workspace that must be zero before first use
 EP_MAX_PARTS = 16            # partial outputs one moe_nvfp4_ep_reduce call sums
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -47,6 +53,7 @@ def _load() -> ctypes.CDLL:
             "`python -m bit_quantized_moe_nvfp4_b200.build` (nvcc, sm_100a)")
     L = ctypes.CDLL(library_path)
     P, I64, SZ, I32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t, ctypes.c_int
+    F32 = ctypes.c_float
     sig = {
         "nvfp4_status_string": (ctypes.c_char_p, [I32]),
         "nvfp4_last_cuda_error": (ctypes.c_char_p, []),
@@ -79,6 +86,18 @@ def _load() -> ctypes.CDLL:
                                                   P, P, P, P, P, P, P, P, SZ, P, P]),
         "moe_nvfp4_forward_w4a4": (I32, [P, P, P, I64, I64, I64, I64, I64,
                                          P, P, P, P, P, P, P, P, SZ, P]),
+        "moe_nvfp4_pre_norm": (I32, [P, P, I64, I64, F32, P, P]),
+        "moe_nvfp4_pre_norm_int8": (I32, [P, P, I64, I64, F32, P, P, P]),
+        "moe_nvfp4_post_norm": (I32, [P, P, P, P, I64, I64, I64, I64, F32, F32, P, P, P, P]),
+        "moe_nvfp4_norm_backward_workspace_size": (SZ, [I64, I64]),
+        "moe_nvfp4_pre_norm_backward": (I32, [P, P, P, P, I64, I64, F32, P, P, P, SZ, P]),
+        "moe_nvfp4_post_norm_backward": (I32, [P, P, P, P, I64, I64, I64, I64, F32, F32,
+                                               P, P, P, P, P, SZ, P]),
+        "moe_nvfp4_gate_up": (I32, [P, P, I64, I64, I64, I32, P, P, P, P]),
+        "moe_nvfp4_gate_up_backward_workspace_size": (SZ, [I64, I64]),
+        "moe_nvfp4_gate_up_backward": (I32, [P, P, P, P, I64, I64, I64, I32, P, P, P, SZ, P, P]),
+        "nvfp4_int8_quantize": (I32, [P, I64, I64, P, P, P]),
+        "nvfp4_int8_matmul": (I32, [P, P, P, P, I64, I64, I64, P, P, P]),
         "moe_nvfp4_shared_workspace_size": (SZ, [I64, I64]),
         "moe_nvfp4_shared_expert": (I32, [P, I64, I64, I64, P, P, P, P, P, SZ, P]),
         "moe_nvfp4_layer_workspace_size": (SZ, [I64, I64, I64, I64, I64, I64]),
@@ -545,6 +564,238 @@ def moe_nvfp4_forward_static(x, topk_ids, topk_w, w_gu, s_gu, g_gu, w_dn, s_dn, 
         _ptr(x), _ptr(topk_ids), _ptr(topk_w), T, H, twoI // 2, E, K, _ptr(w_gu), _ptr(s_gu),
         _ptr(g_gu), _ptr(w_dn), _ptr(s_dn), _ptr(g_dn), _ptr(out),
         _ptr(error_flag) if error_flag is not None else None, _stream(x.device)))
+    return out
+
+
+# ------------------------------------------------------------------------------ dense operators
+def _arg(t, dtype, shape, device, name: str, optional: bool = False):
+    """Address of a contiguous CUDA tensor of this type, shape and device (None: no tensor,
+    where that is allowed)."""
+    if t is None and optional:
+        return None
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.device != device \
+            or tuple(t.shape) != shape or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {shape} "
+                         f"on {device if device.type == 'cuda' else 'a CUDA device'}")
+    return t.data_ptr()
+
+
+def _rows(x, name: str):
+    """(T, H, device) of a two-dimensional tensor."""
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        raise ValueError(f"{name}: expected a two-dimensional tensor")
+    return x.shape[0], x.shape[1], x.device
+
+
+def _new(out, shape, dtype, device, name: str):
+    """(`out` or a new tensor, its address)."""
+    if out is None:
+        out = torch.empty(shape, dtype=dtype, device=device)
+        return out, out.data_ptr()
+    return out, _arg(out, dtype, shape, device, name)
+
+
+def _scratch(workspace, nbytes: int, device):
+    """(workspace, its address, its bytes), allocated when none is given."""
+    if workspace is None:
+        workspace = torch.empty((max(nbytes, 16),), dtype=torch.uint8, device=device)
+    elif not isinstance(workspace, torch.Tensor) or workspace.dtype is not torch.uint8 \
+            or workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace: expected a contiguous torch.uint8 tensor on {device}")
+    return workspace, workspace.data_ptr(), workspace.numel()
+
+
+def _run(name: str, device, *args) -> None:
+    """Call an entry point on the tensors' device and that device's current stream."""
+    f = getattr(_lib(), name)
+    stream = torch.cuda.current_stream(device).cuda_stream
+    if device.index == torch.cuda.current_device():
+        status = f(*args, stream)
+    else:
+        with torch.cuda.device(device):
+            status = f(*args, stream)
+    if status:
+        _check(status)
+
+
+def _flag(error_flag, device):
+    return _arg(error_flag, torch.int32, (1,), device, "error_flag", optional=True)
+
+
+def moe_nvfp4_pre_norm(x, weight, eps: float, out=None) -> torch.Tensor:
+    """weight * x / sqrt(mean(x^2) + eps) for each row of x bf16 [T, H]; weight bf16 [H]."""
+    T, H, dev = _rows(x, "x")
+    px = _arg(x, torch.bfloat16, (T, H), dev, "x")
+    pw = _arg(weight, torch.bfloat16, (H,), dev, "weight")
+    out, po = _new(out, (T, H), torch.bfloat16, dev, "out")
+    _run("moe_nvfp4_pre_norm", dev, px, pw, T, H, eps, po)
+    return out
+
+
+def moe_nvfp4_pre_norm_int8(x, weight, eps: float, codes=None, scales=None):
+    """moe_nvfp4_pre_norm's rows as 8-bit codes and one scale each, for nvfp4_int8_matmul.
+    Returns (codes int8 [T, H], scales fp32 [T])."""
+    T, H, dev = _rows(x, "x")
+    px = _arg(x, torch.bfloat16, (T, H), dev, "x")
+    pw = _arg(weight, torch.bfloat16, (H,), dev, "weight")
+    codes, pc = _new(codes, (T, H), torch.int8, dev, "codes")
+    scales, ps = _new(scales, (T,), torch.float32, dev, "scales")
+    _run("moe_nvfp4_pre_norm_int8", dev, px, pw, T, H, eps, pc, ps)
+    return codes, scales
+
+
+def _gate(gate, T, H, dev):
+    if gate is None:
+        return None, 0, 0
+    rows, cols, _ = _rows(gate, "gate")
+    if rows not in (1, T) or cols not in (1, H):
+        raise ValueError(f"gate: expected a shape that broadcasts to {(T, H)}")
+    return _arg(gate, torch.bfloat16, (rows, cols), dev, "gate"), rows, cols
+
+
+def moe_nvfp4_post_norm(y, weight, residual, eps: float, gate=None, residual_scale: float = 1.0,
+                        next_weight=None, out=None, next_out=None):
+    """out = residual_scale * residual + gate * norm(y), with the norm of moe_nvfp4_pre_norm;
+    gate bf16 [1 or T, 1 or H] or None.  With next_weight [H] also the following block's
+    pre-norm of out.  Returns out bf16 [T, H], or (out, next)."""
+    T, H, dev = _rows(y, "y")
+    bf = torch.bfloat16
+    py = _arg(y, bf, (T, H), dev, "y")
+    pw = _arg(weight, bf, (H,), dev, "weight")
+    pr = _arg(residual, bf, (T, H), dev, "residual")
+    pg, rows, cols = _gate(gate, T, H, dev)
+    pn = _arg(next_weight, bf, (H,), dev, "next_weight", optional=True)
+    if pn is None and next_out is not None:
+        raise ValueError("next_out needs next_weight")
+    out, po = _new(out, (T, H), bf, dev, "out")
+    po2 = None
+    if pn is not None:
+        next_out, po2 = _new(next_out, (T, H), bf, dev, "next_out")
+    _run("moe_nvfp4_post_norm", dev, py, pw, pr, pg, T, H, rows, cols, eps, residual_scale, pn,
+         po, po2)
+    return out if pn is None else (out, next_out)
+
+
+def moe_nvfp4_norm_backward_workspace_size(T: int, H: int) -> int:
+    return int(_lib().moe_nvfp4_norm_backward_workspace_size(T, H))
+
+
+def moe_nvfp4_pre_norm_backward(dy, x, weight, eps: float, dskip=None, dx=None, dweight=None,
+                                workspace=None):
+    """Gradients of moe_nvfp4_pre_norm; dskip [T, H] (the gradient that reaches x past the
+    block) is added to dx.  Returns (dx bf16 [T, H], dweight bf16 [H])."""
+    T, H, dev = _rows(x, "x")
+    bf = torch.bfloat16
+    pd = _arg(dy, bf, (T, H), dev, "dy")
+    px = _arg(x, bf, (T, H), dev, "x")
+    pw = _arg(weight, bf, (H,), dev, "weight")
+    ps = _arg(dskip, bf, (T, H), dev, "dskip", optional=True)
+    dx, pdx = _new(dx, (T, H), bf, dev, "dx")
+    dweight, pdw = _new(dweight, (H,), bf, dev, "dweight")
+    workspace, pws, nws = _scratch(workspace, _norm_scratch(T, H, dev), dev)
+    _run("moe_nvfp4_pre_norm_backward", dev, pd, px, pw, ps, T, H, eps, pdx, pdw, pws, nws)
+    return dx, dweight
+
+
+def _norm_scratch(T, H, dev):
+    if dev.index == torch.cuda.current_device():
+        return _lib().moe_nvfp4_norm_backward_workspace_size(T, H)
+    with torch.cuda.device(dev):
+        return _lib().moe_nvfp4_norm_backward_workspace_size(T, H)
+
+
+def moe_nvfp4_post_norm_backward(dout, y, weight, eps: float, gate=None,
+                                 residual_scale: float = 1.0, dy=None, dweight=None, dgate=None,
+                                 dresidual=None, need_dresidual: bool = True, workspace=None):
+    """Gradients of moe_nvfp4_post_norm's out.  Returns (dy bf16 [T, H], dweight bf16 [H],
+    dgate of gate's shape or None without a gate, dresidual bf16 [T, H] or None when
+    need_dresidual is false)."""
+    T, H, dev = _rows(y, "y")
+    bf = torch.bfloat16
+    pd = _arg(dout, bf, (T, H), dev, "dout")
+    py = _arg(y, bf, (T, H), dev, "y")
+    pw = _arg(weight, bf, (H,), dev, "weight")
+    pg, rows, cols = _gate(gate, T, H, dev)
+    dy, pdy = _new(dy, (T, H), bf, dev, "dy")
+    dweight, pdw = _new(dweight, (H,), bf, dev, "dweight")
+    pdg = pdr = None
+    if gate is not None:
+        dgate, pdg = _new(dgate, (rows, cols), bf, dev, "dgate")
+    elif dgate is not None:
+        raise ValueError("dgate needs gate")
+    if need_dresidual or dresidual is not None:
+        dresidual, pdr = _new(dresidual, (T, H), bf, dev, "dresidual")
+    workspace, pws, nws = _scratch(workspace, _norm_scratch(T, H, dev), dev)
+    _run("moe_nvfp4_post_norm_backward", dev, pd, py, pw, pg, T, H, rows, cols, eps,
+         residual_scale, pdy, pdw, pdg, pdr, pws, nws)
+    return dy, dweight, dgate, dresidual
+
+
+def moe_nvfp4_gate_up(x, w_gu, act: int = ACT_SILU, h=None, gu=None,
+                      error_flag=None) -> torch.Tensor:
+    """h = act(x W_g^T) * (x W_u^T) in one kernel; x bf16 [T, H]; w_gu bf16 [2I, H], gate rows
+    first.  gu bf16 [T, 2I], when given, receives the pre-activations that
+    moe_nvfp4_gate_up_backward takes.  Returns h bf16 [T, I]."""
+    T, H, dev = _rows(x, "x")
+    bf = torch.bfloat16
+    I = _rows(w_gu, "w_gu")[0] // 2
+    px = _arg(x, bf, (T, H), dev, "x")
+    pw = _arg(w_gu, bf, (2 * I, H), dev, "w_gu")
+    h, ph = _new(h, (T, I), bf, dev, "h")
+    pgu = _arg(gu, bf, (T, 2 * I), dev, "gu", optional=True)
+    _run("moe_nvfp4_gate_up", dev, px, pw, T, H, I, act, ph, pgu, _flag(error_flag, dev))
+    return h
+
+
+def moe_nvfp4_gate_up_backward_workspace_size(T: int, I: int) -> int:
+    return int(_lib().moe_nvfp4_gate_up_backward_workspace_size(T, I))
+
+
+def moe_nvfp4_gate_up_backward(dh, x, w_gu, gu, act: int = ACT_SILU, dx=None, dw_gu=None,
+                               need_dx: bool = True, need_dw: bool = True, workspace=None,
+                               error_flag=None):
+    """Gradients of moe_nvfp4_gate_up from dh bf16 [T, I] and the kept gu.  Returns
+    (dx bf16 [T, H], dw_gu bf16 [2I, H]), None in the place of one that is not needed."""
+    T, H, dev = _rows(x, "x")
+    bf = torch.bfloat16
+    I = _rows(w_gu, "w_gu")[0] // 2
+    pd = _arg(dh, bf, (T, I), dev, "dh")
+    px = _arg(x, bf, (T, H), dev, "x")
+    pw = _arg(w_gu, bf, (2 * I, H), dev, "w_gu")
+    pgu = _arg(gu, bf, (T, 2 * I), dev, "gu")
+    pdx = pdw = None
+    if need_dx or dx is not None:
+        dx, pdx = _new(dx, (T, H), bf, dev, "dx")
+    if need_dw or dw_gu is not None:
+        dw_gu, pdw = _new(dw_gu, (2 * I, H), bf, dev, "dw_gu")
+    workspace, pws, nws = _scratch(workspace, 4 * T * I + 256, dev)
+    _run("moe_nvfp4_gate_up_backward", dev, pd, px, pw, pgu, T, H, I, act, pdx, pdw, pws, nws,
+         _flag(error_flag, dev))
+    return dx, dw_gu
+
+
+def nvfp4_int8_quantize(x, codes=None, scales=None):
+    """Rows of x bf16 [rows, cols] -> (codes int8 [rows, cols], scales fp32 [rows]):
+    scale = max |x| / 127, code = the integer nearest to x / scale."""
+    T, K, dev = _rows(x, "x")
+    px = _arg(x, torch.bfloat16, (T, K), dev, "x")
+    codes, pc = _new(codes, (T, K), torch.int8, dev, "codes")
+    scales, ps = _new(scales, (T,), torch.float32, dev, "scales")
+    _run("nvfp4_int8_quantize", dev, px, T, K, pc, ps)
+    return codes, scales
+
+
+def nvfp4_int8_matmul(a, a_scales, w, w_scales, out=None, error_flag=None) -> torch.Tensor:
+    """bf16 [T, N] = (a [T, K] int8 times w [N, K] int8 transposed, exact) scaled by a_scales
+    fp32 [T] and w_scales fp32 [N]."""
+    T, K, dev = _rows(a, "a")
+    N = _rows(w, "w")[0]
+    pa = _arg(a, torch.int8, (T, K), dev, "a")
+    pw = _arg(w, torch.int8, (N, K), dev, "w")
+    pas = _arg(a_scales, torch.float32, (T,), dev, "a_scales")
+    pws = _arg(w_scales, torch.float32, (N,), dev, "w_scales")
+    out, po = _new(out, (T, N), torch.bfloat16, dev, "out")
+    _run("nvfp4_int8_matmul", dev, pa, pas, pw, pws, T, N, K, po, _flag(error_flag, dev))
     return out
 
 

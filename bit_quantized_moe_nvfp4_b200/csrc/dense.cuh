@@ -1,0 +1,633 @@
+// dense.cuh -- dense tensor-core products D = A B^T (tcgen05, sm_100a) with the epilogues of
+// the 8-bit product (int8.cu) and of the gated projection and its gradients (gate_up.cu).
+//
+// Operands are 16-bit floats (fp32 sums) or 8-bit integers (exact int32 sums).  Each comes by
+// TMA into a ring of 128-byte-swizzled stages, K-major ([rows, K], as weights and activations
+// lie in memory) or, for 16-bit types, MN-major ([K, rows]: the transposed operands of the
+// gradients, so nothing is ever transposed in memory).  What lies outside a tensor reads as
+// zero, so no size has to be a multiple of a tile.  Two kernels:
+//
+//  * dense_pair_kernel, large products: pairs of CTAs (cta_group::2) each take 256 x 256
+//    tiles.  Every CTA holds 128 rows of A and 128 rows of B a stage, so the pair reads half
+//    the shared memory per flop that two single CTAs would.  Tiles are handed out in a fixed
+//    order; two TMEM accumulators let the epilogue of a tile run under the next one's MMAs.
+//  * dense_split_kernel, few tokens or small matrices: 128 x NT tiles of one CTA, the sum
+//    over K split over the CTAs of a cluster so that every SM streams its share of the
+//    weights.  Partial tiles meet in shared memory: each CTA adds its slice of the tile over
+//    the cluster's CTAs in rank order (the result does not depend on timing) and stores it.
+//
+// Every wait is bounded; one that gives up ORs bit 1 into the caller's error flag.
+#pragma once
+#include <algorithm>
+
+#include "moe.cuh"
+#include "tcgen05.cuh"
+
+namespace nvfp4 {
+
+enum DenseKind { kBf16 = 0, kS8 = 1 };
+enum DenseEpi { kEpiStore = 0, kEpiScale = 1, kEpiGate = 2 };
+
+// act(z) and its slope: SiLU, or GELU by its tanh form.
+__device__ __forceinline__ float tanh_f32(float v) {
+  const float e = expf(-2.f * fabsf(v));
+  return copysignf((1.f - e) / (1.f + e), v);
+}
+template <int ACT>
+__device__ __forceinline__ float gate_act(float z) {
+  if (ACT == NVFP4_ACT_SILU) return silu_f32(z);
+  return 0.5f * z * (1.f + tanh_f32(0.7978845608028654f * fmaf(0.044715f * z * z, z, z)));
+}
+
+struct DenseArgs {
+  // Logical product: D[m, n] = sum_k A[m, k] B[n, k].  pair kernel: D rows are the output's
+  // rows.  split kernel: D rows are the output's columns unless `row_major_d`.
+  int64_t M, N, K;
+  int64_t half;                // kEpiGate: I, the rows of the gate half of w_gu
+  const float *m_scale;        // kEpiScale: scale of each D row
+  const float *n_scale;        //            scale of each D column
+  __nv_bfloat16 *out;          // split kernel: output, `ld` elements a row
+  __nv_bfloat16 *gu;           // split kernel, kEpiGate: [cols, 2 half] pre-activations, or null
+  int64_t ld;
+  int row_major_d;             // split kernel: out[m * ld + n] instead of out[n * ld + m]
+  int save_gu;                 // pair kernel, kEpiGate: tensor maps g / u are set
+  int32_t *flag;               // error bits, or null
+  int m_tiles, n_tiles;
+};
+
+// Bounded wait of one CTA; after any of its waits has given up, later ones return at once.
+struct CtaWait {
+  int *abort;
+  int32_t *flag;
+  __device__ __forceinline__ bool operator()(uint64_t *bar, uint32_t parity) const {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*(volatile int *)abort) return false;
+    if (mbar_wait(bar, parity)) return true;
+    *(volatile int *)abort = 1;
+    report_timeout(flag);
+    return false;
+  }
+};
+
+// ------------------------------------------------------------------ pairs of CTAs
+constexpr int kPS = 6;                              // stages
+constexpr uint32_t kPHalf = 128 * 128;              // A or B part of a stage, one CTA
+constexpr uint32_t kPStage = 2 * kPHalf;
+constexpr uint32_t kPOut = kPS * kPStage;           // 4 warps x 2 buffers of 32 rows x 128 B
+constexpr uint32_t kPBars = kPOut + 4 * 2 * 4096;
+constexpr uint32_t kPMisc = kPBars + 8 * (2 * kPS + 4);
+constexpr uint32_t kPSmem = kPMisc + 16 + 1024;
+constexpr int kPThreads = 192;                      // producer, MMA, 4 epilogue warps
+static_assert(kPSmem <= 227 * 1024, "shared memory budget");
+
+// Tile `i` of m_tiles x n_tiles, in groups of 8 rows of tiles, so that the tiles in flight at
+// one time share A and B tiles in L2.
+__device__ __forceinline__ void tile_at(int i, int m_tiles, int n_tiles, int &mt, int &nt) {
+  const int per = 8 * n_tiles, g = i / per, r = i % per;
+  const int rows = min(8, m_tiles - g * 8);
+  mt = g * 8 + r % rows;
+  nt = r / rows;
+}
+
+// One 128-byte-wide chunk (64 bf16 columns) of a warp's 32 rows: packed values -> swizzled
+// staging buffer -> TMA store (rows and columns outside the tensor are not written).
+__device__ __forceinline__ void store_chunk(const uint32_t (&v)[32], unsigned char *buf, int lane,
+                                            const CUtensorMap *map, int x, int y, bool inside) {
+  if (lane == 0) bulk_wait_group_read<1>();   // the store before the last has left this buffer
+  __syncwarp();
+#pragma unroll
+  for (int c = 0; c < 8; ++c)
+    *reinterpret_cast<uint4 *>(buf + lane * 128 + ((c ^ (lane & 7)) << 4)) =
+        make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) {
+    if (inside) tma_store_2d(map, x, y, buf);
+    bulk_commit_group();
+  }
+}
+
+template <int KIND, bool AMN, bool BMN, int EPI, int ACT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
+    dense_pair_kernel(const __grid_constant__ CUtensorMap map_a,
+                      const __grid_constant__ CUtensorMap map_b,
+                      const __grid_constant__ CUtensorMap map_out,
+                      const __grid_constant__ CUtensorMap map_g,
+                      const __grid_constant__ CUtensorMap map_u, DenseArgs p) {
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  //   full[s]      (leader's) both CTAs' tiles of stage s have landed
+  //   freeb[s]     the MMAs reading stage s are done (commit, to both CTAs)
+  //   accfull[b]   accumulator b holds a finished tile (commit, to both CTAs)
+  //   accempty[b]  (leader's) the 8 epilogue warps have read accumulator b
+  uint64_t *full = reinterpret_cast<uint64_t *>(smem + kPBars);
+  uint64_t *freeb = full + kPS;
+  uint64_t *accfull = freeb + kPS;
+  uint64_t *accempty = accfull + 2;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + kPMisc);
+  int *abort = reinterpret_cast<int *>(smem + kPMisc + 4);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = (int)cluster_rank();
+
+  if (threadIdx.x == 0) {
+    *abort = 0;
+    for (int s = 0; s < kPS; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&freeb[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&accfull[b], 1);
+      mbar_init(&accempty[b], 8);
+    }
+    mbar_init_fence();
+  }
+  if (warp == 1) tmem_alloc_pair(tmem_slot, 512);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();   // the peer's barriers exist before anything arrives on them
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  pdl_wait();
+
+  const CtaWait wait{abort, p.flag};
+  const int total = p.m_tiles * p.n_tiles, pairs = (int)gridDim.x / 2;
+  const int first = (int)blockIdx.x / 2;
+  constexpr int kElems = KIND == kS8 ? 128 : 64;   // K elements of a stage
+  const int kblocks = (int)((p.K + kElems - 1) / kElems);
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int kg = 0;
+      for (int i = first; i < total; i += pairs) {
+        int mt, nt;
+        tile_at(i, p.m_tiles, p.n_tiles, mt, nt);
+        const int m0 = mt * 256 + rank * 128;
+        const int n0 = EPI == kEpiGate ? (int)(rank * p.half + nt * 128) : nt * 256 + rank * 128;
+        for (int kb = 0; kb < kblocks; ++kb, ++kg) {
+          const int s = kg % kPS;
+          if (kg >= kPS && !wait(&freeb[s], ((kg / kPS) - 1) & 1)) break;
+          if (*(volatile int *)abort) break;
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * kPStage);
+          const uint32_t bar = map_rank(smem_u32(&full[s]), 0);
+          unsigned char *A = smem + s * kPStage, *B = A + kPHalf;
+          const int k0 = kb * kElems;
+          if (AMN) {
+            tma_load_2d_pair(A, &map_a, m0, k0, bar);
+            tma_load_2d_pair(A + kPHalf / 2, &map_a, m0 + 64, k0, bar);
+          } else {
+            tma_load_2d_pair(A, &map_a, k0, m0, bar);
+          }
+          if (BMN) {
+            tma_load_2d_pair(B, &map_b, n0, k0, bar);
+            tma_load_2d_pair(B + kPHalf / 2, &map_b, n0 + 64, k0, bar);
+          } else {
+            tma_load_2d_pair(B, &map_b, k0, n0, bar);
+          }
+        }
+        if (*(volatile int *)abort) break;
+      }
+      // the leader sees both CTAs' copies land; the peer stays until then (cluster_sync)
+      if (rank == 0)
+        for (int t = max(0, kg - kPS); t < kg; ++t) mbar_wait(&full[t % kPS], (t / kPS) & 1);
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      constexpr uint32_t idesc =
+          (KIND == kS8 ? idesc_s8_s32(256, 256) : idesc_bf16_f32(256, 256)) |
+          (AMN ? kIdescMnMajorA : 0) | (BMN ? kIdescMnMajorB : 0);
+      int kg = 0, tc = 0;
+      for (int i = first; i < total; i += pairs, ++tc) {
+        const int acc = tc & 1;
+        if (tc >= 2 && !wait(&accempty[acc], ((tc >> 1) - 1) & 1)) break;
+        tc_fence_after();
+        const uint32_t d = tmem_base + acc * 256;
+        for (int kb = 0; kb < kblocks; ++kb, ++kg) {
+          const int s = kg % kPS;
+          const bool ok = wait(&full[s], (kg / kPS) & 1);
+          tc_fence_after();
+          if (ok) {
+            const uint32_t a = smem_u32(smem + s * kPStage);
+            const uint64_t da = AMN ? smem_desc_mn_sw128(a, kPHalf / 2) : smem_desc_sw128(a);
+            const uint64_t db = BMN ? smem_desc_mn_sw128(a + kPHalf, kPHalf / 2)
+                                    : smem_desc_sw128(a + kPHalf);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+              // 32 bytes along the rows (K-major), or 16 K rows of 128 bytes (MN-major)
+              const uint64_t ak = da + (AMN ? 128 : 2) * kk, bk = db + (BMN ? 128 : 2) * kk;
+              if (KIND == kS8)
+                umma_s8_pair(d, ak, bk, idesc, kb > 0 || kk > 0);
+              else
+                umma_bf16_pair(d, ak, bk, idesc, kb > 0 || kk > 0);
+            }
+          }
+          umma_commit_pair(&freeb[s]);
+        }
+        umma_commit_pair(&accfull[acc]);
+      }
+    }
+  } else {
+    const int q = warp & 3;
+    unsigned char *buf = smem + kPOut + (warp - 2) * 8192;
+    int tc = 0, nst = 0;
+    for (int i = first; i < total; i += pairs, ++tc) {
+      int mt, nt;
+      tile_at(i, p.m_tiles, p.n_tiles, mt, nt);
+      const int acc = tc & 1;
+      if (!wait(&accfull[acc], (tc >> 1) & 1)) break;
+      tc_fence_after();
+      const uint32_t tb = tmem_base + acc * 256 + ((uint32_t)(q * 32) << 16);
+      const int row0 = mt * 256 + rank * 128 + q * 32;
+      const bool rows_in = row0 < p.M;
+      if (EPI == kEpiGate) {
+        // columns 0..127 gate, 128..255 up, of the same 128 columns of h
+        for (int c = 0; c < 2; ++c) {
+          const int x = nt * 128 + c * 64;
+          uint32_t hp[32], gp[32], up[32];
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            uint32_t g[32], u[32];
+            tmem_ld32(tb + c * 64 + hf * 32, g);
+            tmem_ld32(tb + 128 + c * 64 + hf * 32, u);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              const float g0 = __uint_as_float(g[2 * k]), g1 = __uint_as_float(g[2 * k + 1]);
+              const float u0 = __uint_as_float(u[2 * k]), u1 = __uint_as_float(u[2 * k + 1]);
+              hp[hf * 16 + k] = pack_bf16x2(gate_act<ACT>(g0) * u0, gate_act<ACT>(g1) * u1);
+              gp[hf * 16 + k] = pack_bf16x2(g0, g1);
+              up[hf * 16 + k] = pack_bf16x2(u0, u1);
+            }
+          }
+          const bool in = rows_in && x < p.N;
+          store_chunk(hp, buf + (nst++ & 1) * 4096, lane, &map_out, x, row0, in);
+          if (p.save_gu) {
+            store_chunk(gp, buf + (nst++ & 1) * 4096, lane, &map_g, x, row0, in);
+            store_chunk(up, buf + (nst++ & 1) * 4096, lane, &map_u, x, row0, in);
+          }
+        }
+      } else {
+        const int row = row0 + lane;
+        const float ms = (EPI == kEpiScale && row < p.M) ? __ldg(p.m_scale + row) : 0.f;
+        for (int c = 0; c < 4; ++c) {
+          const int x = nt * 256 + c * 64;
+          uint32_t o[32];
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            uint32_t v[32];
+            tmem_ld32(tb + c * 64 + hf * 32, v);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              float f[4];
+              if (EPI == kEpiScale) {
+                const int col = x + hf * 32 + k * 4;
+                const float4 ns = col < p.N ? __ldg(reinterpret_cast<const float4 *>(p.n_scale + col))
+                                            : make_float4(0.f, 0.f, 0.f, 0.f);
+                f[0] = (float)(int)v[4 * k] * ms * ns.x;
+                f[1] = (float)(int)v[4 * k + 1] * ms * ns.y;
+                f[2] = (float)(int)v[4 * k + 2] * ms * ns.z;
+                f[3] = (float)(int)v[4 * k + 3] * ms * ns.w;
+              } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) f[j] = __uint_as_float(v[4 * k + j]);
+              }
+              o[hf * 16 + 2 * k] = pack_bf16x2(f[0], f[1]);
+              o[hf * 16 + 2 * k + 1] = pack_bf16x2(f[2], f[3]);
+            }
+          }
+          store_chunk(o, buf + (nst++ & 1) * 4096, lane, &map_out, x, row0, rows_in && x < p.N);
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(map_rank(smem_u32(&accempty[acc]), 0));
+    }
+    if (lane == 0) bulk_wait_group_all();
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  pdl_launch_dependents();
+  cluster_sync();   // the leader's MMAs read the peer's shared memory until here
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, 512);
+  }
+  cluster_sync();   // both CTAs are there for the deallocation
+}
+
+// ------------------------------------------------------------------ K split over a cluster
+constexpr int kSThreads = 256;   // producer, MMA, 4 TMEM warps; all 8 add and store
+template <int NT>
+struct SplitShape {
+  static constexpr int kStages = NT == 16 ? 5 : NT == 32 ? 5 : NT == 64 ? 4 : NT == 128 ? 3 : 4;
+  static constexpr uint32_t kA = 128 * 128, kB = NT * 128, kStage = kA + kB;
+  // partial tile, fp32 or int32: [NT][128], or [128][NT + 4] for a row-major D
+  static constexpr uint32_t kRed = 128 * (NT + 4) * 4;
+  static constexpr uint32_t kRing = kStages * kStage > kRed ? kStages * kStage : kRed;
+  static constexpr uint32_t kBars = (kRing + 15) / 16 * 16;
+  static constexpr uint32_t kMisc = kBars + 8 * (2 * kStages + 1);
+  static constexpr uint32_t kSmem = kMisc + 16 + 1024;
+  static constexpr uint32_t kTmemCols = NT < 32 ? 32 : NT;
+};
+
+__device__ __forceinline__ float2 ld_cluster_f2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr));
+  return v;
+}
+
+template <int KIND, bool AMN, bool BMN, int EPI, int ACT, int NT>
+__global__ void __launch_bounds__(kSThreads)
+    dense_split_kernel(const __grid_constant__ CUtensorMap map_a,
+                       const __grid_constant__ CUtensorMap map_b, DenseArgs p) {
+  using S = SplitShape<NT>;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  uint64_t *full = reinterpret_cast<uint64_t *>(smem + S::kBars);
+  uint64_t *freeb = full + S::kStages;
+  uint64_t *accfull = freeb + S::kStages;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + S::kMisc);
+  int *abort = reinterpret_cast<int *>(smem + S::kMisc + 4);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = (int)cluster_rank(), nr = (int)cluster_size();
+
+  if (threadIdx.x == 0) {
+    *abort = 0;
+    for (int s = 0; s < S::kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&freeb[s], 1);
+    }
+    mbar_init(accfull, 1);
+    mbar_init_fence();
+  }
+  if (warp == 1) tmem_alloc(tmem_slot, S::kTmemCols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  pdl_launch_dependents();
+  pdl_wait();
+
+  const CtaWait wait{abort, p.flag};
+  constexpr int kElems = KIND == kS8 ? 128 : 64;
+  const int kblocks = (int)((p.K + kElems - 1) / kElems);
+  const int kb0 = (int)((int64_t)rank * kblocks / nr), kb1 = (int)((int64_t)(rank + 1) * kblocks / nr);
+  const int tile = (int)blockIdx.x / nr, mt = tile % p.m_tiles, nt = tile / p.m_tiles;
+  constexpr int kTileM = EPI == kEpiGate ? 64 : 128;   // output columns (D rows) of a tile
+  const int m0 = mt * kTileM, n0 = nt * NT;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int i = 0;
+      for (int kb = kb0; kb < kb1; ++kb, ++i) {
+        const int s = i % S::kStages;
+        if (i >= S::kStages && !wait(&freeb[s], ((i / S::kStages) - 1) & 1)) break;
+        mbar_arrive_expect_tx(&full[s], S::kStage);
+        unsigned char *A = smem + s * S::kStage, *B = A + S::kA;
+        const int k0 = kb * kElems;
+        if (EPI == kEpiGate) {   // 64 gate rows, then the matching 64 up rows
+          tma_load_2d(A, &map_a, k0, m0, &full[s]);
+          tma_load_2d(A + S::kA / 2, &map_a, k0, (int)p.half + m0, &full[s]);
+        } else if (AMN) {
+          tma_load_2d(A, &map_a, m0, k0, &full[s]);
+          tma_load_2d(A + S::kA / 2, &map_a, m0 + 64, k0, &full[s]);
+        } else {
+          tma_load_2d(A, &map_a, k0, m0, &full[s]);
+        }
+        if (BMN) {
+#pragma unroll
+          for (int j = 0; j < NT / 64; ++j)
+            tma_load_2d(B + j * 8192, &map_b, n0 + 64 * j, k0, &full[s]);
+        } else {
+          tma_load_2d(B, &map_b, k0, n0, &full[s]);
+        }
+      }
+      // every copy lands before the ring is used again or the CTA exits
+      for (int t = max(0, i - S::kStages); t < i; ++t)
+        mbar_wait(&full[t % S::kStages], (t / S::kStages) & 1);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      constexpr uint32_t idesc = (KIND == kS8 ? idesc_s8_s32(128, NT) : idesc_bf16_f32(128, NT)) |
+                                 (AMN ? kIdescMnMajorA : 0) | (BMN ? kIdescMnMajorB : 0);
+      for (int i = 0; i < kb1 - kb0; ++i) {
+        const int s = i % S::kStages;
+        const bool ok = wait(&full[s], (i / S::kStages) & 1);
+        tc_fence_after();
+        if (ok) {
+          const uint32_t a = smem_u32(smem + s * S::kStage);
+          const uint64_t da = AMN ? smem_desc_mn_sw128(a, S::kA / 2) : smem_desc_sw128(a);
+          const uint64_t db =
+              BMN ? smem_desc_mn_sw128(a + S::kA, 8192) : smem_desc_sw128(a + S::kA);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            const uint64_t ak = da + (AMN ? 128 : 2) * kk, bk = db + (BMN ? 128 : 2) * kk;
+            if (KIND == kS8)
+              umma_s8(tmem_base, ak, bk, idesc, i > 0 || kk > 0);
+            else
+              umma_bf16(tmem_base, ak, bk, idesc, i > 0 || kk > 0);
+          }
+        }
+        umma_commit(&freeb[s]);
+      }
+      umma_commit(accfull);
+    }
+  }
+  __syncwarp();
+  // every thread of the CTA waits for the tile: the ring is free and may hold partial sums
+  const bool done = wait(accfull, 0);
+  __syncthreads();   // the producer's copies have landed too
+  tc_fence_after();
+  uint32_t *red = reinterpret_cast<uint32_t *>(smem);
+  constexpr int kRowPitch = NT + 4;
+  if (warp >= 4) {
+    const int q = warp & 3, row = q * 32 + lane;
+    const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16);
+    const bool any = done && kb1 > kb0;
+#pragma unroll 1
+    for (int c = 0; c < NT; c += 16) {
+      uint32_t v[16];
+      tmem_ld16(tb + c, v);
+      if (!any)
+#pragma unroll
+        for (int k = 0; k < 16; ++k) v[k] = 0;
+      if (p.row_major_d) {
+#pragma unroll
+        for (int k = 0; k < 16; k += 4)
+          *reinterpret_cast<uint4 *>(red + row * kRowPitch + c + k) =
+              make_uint4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 16; ++k) red[(c + k) * 128 + row] = v[k];
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, S::kTmemCols);
+  }
+  cluster_sync();
+  // Add the cluster's partial tiles: pairs of neighbouring values, this CTA's share of them.
+  const uint32_t base = smem_u32(red);
+  auto sum_at = [&](int at) {   // `at`: index of an even element of the partial tile
+    float2 v = make_float2(0.f, 0.f);
+    if (KIND == kS8) {
+      int a = 0, b = 0;
+      for (int r = 0; r < nr; ++r) {
+        const float2 w = ld_cluster_f2(map_rank(base + at * 4, r));
+        a += __float_as_int(w.x);
+        b += __float_as_int(w.y);
+      }
+      v = make_float2((float)a, (float)b);
+    } else {
+      for (int r = 0; r < nr; ++r) {
+        const float2 w = ld_cluster_f2(map_rank(base + at * 4, r));
+        v.x += w.x;
+        v.y += w.y;
+      }
+    }
+    return v;
+  };
+  if (p.row_major_d) {
+    const int pairs = 128 * (NT / 2);
+    const int e0 = (int)((int64_t)pairs * rank / nr), e1 = (int)((int64_t)pairs * (rank + 1) / nr);
+    for (int e = e0 + (int)threadIdx.x; e < e1; e += kSThreads) {
+      const int m = e / (NT / 2), n = e % (NT / 2) * 2;
+      if (m0 + m < p.M && n0 + n < p.N) {   // N is even
+        const float2 v = sum_at(m * kRowPitch + n);
+        *reinterpret_cast<uint32_t *>(p.out + (int64_t)(m0 + m) * p.ld + n0 + n) =
+            pack_bf16x2(v.x, v.y);
+      }
+    }
+  } else {
+    const int cols = (int)min((int64_t)NT, p.N - n0);   // tokens of this tile
+    const int pairs = cols * (kTileM / 2);
+    const int e0 = (int)((int64_t)pairs * rank / nr), e1 = (int)((int64_t)pairs * (rank + 1) / nr);
+    for (int e = e0 + (int)threadIdx.x; e < e1; e += kSThreads) {
+      const int n = e / (kTileM / 2), m = e % (kTileM / 2) * 2;
+      if (m0 + m >= p.M) continue;   // M is even
+      float2 v = sum_at(n * 128 + m);
+      const int64_t row = n0 + n;
+      if (EPI == kEpiGate) {
+        const float2 u = sum_at(n * 128 + 64 + m);
+        if (p.gu) {
+          uint32_t *o = reinterpret_cast<uint32_t *>(p.gu + row * 2 * p.half + m0 + m);
+          o[0] = pack_bf16x2(v.x, v.y);
+          o[p.half / 2] = pack_bf16x2(u.x, u.y);
+        }
+        v.x = gate_act<ACT>(v.x) * u.x;
+        v.y = gate_act<ACT>(v.y) * u.y;
+      } else if (EPI == kEpiScale) {
+        const float ts = __ldg(p.n_scale + row);
+        v.x = v.x * ts * __ldg(p.m_scale + m0 + m);
+        v.y = v.y * ts * __ldg(p.m_scale + m0 + m + 1);
+      }
+      *reinterpret_cast<uint32_t *>(p.out + row * p.ld + m0 + m) = pack_bf16x2(v.x, v.y);
+    }
+  }
+  cluster_sync();   // no CTA leaves while another still reads its partial tile
+}
+
+// ------------------------------------------------------------------ host side
+// Tensor map of a 16- or 8-bit operand: K-major [rows, K] (boxes of box_rows rows by 128
+// bytes), or MN-major [K, rows] (boxes of 64 K rows by 64 values).
+inline int operand_map(CUtensorMap *m, int kind, bool mn, const void *base, int64_t rows,
+                       int64_t K, int box_rows) {
+  const CUtensorMapDataType t =
+      kind == kS8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const int bytes = kind == kS8 ? 1 : 2;
+  int st = mn ? make_map(m, t, bytes, base, (uint64_t)rows, (uint64_t)K, 64, 64,
+                         CU_TENSOR_MAP_SWIZZLE_128B)
+              : make_map(m, t, bytes, base, (uint64_t)K, (uint64_t)rows, 128 / bytes,
+                         (uint32_t)box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (st) set_last_cuda_error(cudaErrorInvalidValue);
+  return st;
+}
+// Tensor map of an output: `cols` bf16 of rows `ld` elements apart, boxes of 32 rows x 64.
+inline int out_map(CUtensorMap *m, const void *base, int64_t rows, int64_t cols, int64_t ld) {
+  int st = make_map_pitch(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, (uint64_t)cols,
+                          (uint64_t)rows, (uint64_t)ld * 2, 64, 32, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (st) set_last_cuda_error(cudaErrorInvalidValue);
+  return st;
+}
+
+// Whether a [rows, cols] result goes to the pair kernel: when its 256 x 256 tiles keep at least
+// half of the CTA pairs busy.
+inline bool dense_use_pair(int64_t rows, int64_t cols) {
+  return ceil_div(rows, 256) * ceil_div(cols, 256) * 4 >= num_sms();
+}
+
+// Where the operands lie: A [M, K] (or [K, M]) and B [N, K] (or [K, N]).
+struct DenseOperands {
+  const void *a, *b;
+};
+
+template <int KIND, bool AMN, bool BMN, int EPI, int ACT>
+int launch_pair(DenseArgs p, DenseOperands o, const CUtensorMap &out, const CUtensorMap &g,
+                const CUtensorMap &u, cudaStream_t s) {
+  CUtensorMap ta, tb;
+  const int64_t brows = EPI == kEpiGate ? 2 * p.half : p.N;
+  if (int st = operand_map(&ta, KIND, AMN, o.a, p.M, p.K, 128)) return st;
+  if (int st = operand_map(&tb, KIND, BMN, o.b, brows, p.K, 128)) return st;
+  p.m_tiles = (int)ceil_div(p.M, 256);
+  p.n_tiles = (int)ceil_div(p.N, EPI == kEpiGate ? 128 : 256);
+  auto k = dense_pair_kernel<KIND, AMN, BMN, EPI, ACT>;
+  if (resident_blocks(k, kPThreads, kPSmem) < 0) return NVFP4_ECUDA;
+  const int total = p.m_tiles * p.n_tiles;
+  const int pairs = std::min(total, num_sms() / 2);
+  return launch_pdl(k, dim3(2 * pairs), dim3(kPThreads), kPSmem, s, ta, tb, out, g, u, p);
+}
+
+template <int KIND, bool AMN, bool BMN, int EPI, int ACT, int NT>
+int launch_split(DenseArgs p, DenseOperands o, cudaStream_t s) {
+  using S = SplitShape<NT>;
+  static_assert(S::kSmem <= 227 * 1024, "shared memory budget");
+  CUtensorMap ta, tb;
+  const int64_t arows = EPI == kEpiGate ? 2 * p.half : p.M;
+  if (int st = operand_map(&ta, KIND, AMN, o.a, arows, p.K, EPI == kEpiGate ? 64 : 128)) return st;
+  if (int st = operand_map(&tb, KIND, BMN, o.b, p.N, p.K, NT)) return st;
+  p.m_tiles = (int)ceil_div(p.M, EPI == kEpiGate ? 64 : 128);
+  p.n_tiles = (int)ceil_div(p.N, NT);
+  auto k = dense_split_kernel<KIND, AMN, BMN, EPI, ACT, NT>;
+  const int res = resident_blocks(k, kSThreads, S::kSmem);
+  if (res <= 0) return NVFP4_ECUDA;
+  const int64_t tiles = (int64_t)p.m_tiles * p.n_tiles;
+  const int64_t kblocks = ceil_div(p.K, KIND == kS8 ? 128 : 64);
+  const int slots = num_sms() * std::min(res, 2);
+  const int nr = (int)std::max<int64_t>(
+      1, std::min<int64_t>({8, slots / tiles, kblocks}));
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(tiles * nr));
+  cfg.blockDim = dim3(kSThreads);
+  cfg.dynamicSmemBytes = S::kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = nr;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, k, ta, tb, p);
+  if (e != cudaSuccess) {
+    set_last_cuda_error(e);
+    return NVFP4_ECUDA;
+  }
+  return NVFP4_OK;
+}
+
+// The split kernel with the smallest column tile that holds N columns, up to MAXNT.
+template <int KIND, bool AMN, bool BMN, int EPI, int ACT>
+int launch_split_n(const DenseArgs &p, DenseOperands o, cudaStream_t s) {
+  if constexpr (!BMN) {
+    if (p.N <= 16) return launch_split<KIND, AMN, BMN, EPI, ACT, 16>(p, o, s);
+    if (p.N <= 32) return launch_split<KIND, AMN, BMN, EPI, ACT, 32>(p, o, s);
+    if (p.N <= 64) return launch_split<KIND, AMN, BMN, EPI, ACT, 64>(p, o, s);
+  }
+  return launch_split<KIND, AMN, BMN, EPI, ACT, 128>(p, o, s);
+}
+
+}  // namespace nvfp4

@@ -619,20 +619,26 @@ static EncodeTiledFn encode_fn() {
   return fn;
 }
 
-// 2-D tiled map over a row-major [rows, cols] array.
-int make_map(CUtensorMap *m, CUtensorMapDataType type, int elem_bytes, const void *base,
-             uint64_t cols, uint64_t rows, uint32_t box_cols, uint32_t box_rows,
-             CUtensorMapSwizzle swz) {
+// 2-D tiled map over a row-major [rows, cols] array whose rows are `pitch` bytes apart.
+int make_map_pitch(CUtensorMap *m, CUtensorMapDataType type, const void *base, uint64_t cols,
+                   uint64_t rows, uint64_t pitch, uint32_t box_cols, uint32_t box_rows,
+                   CUtensorMapSwizzle swz) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return NVFP4_ECUDA;
   const cuuint64_t dims[2] = {cols, rows};
-  const cuuint64_t strides[1] = {cols * elem_bytes};
+  const cuuint64_t strides[1] = {pitch};
   const cuuint32_t box[2] = {box_cols, box_rows};
   const cuuint32_t estr[2] = {1, 1};
   CUresult r = fn(m, type, 2, const_cast<void *>(base), dims, strides, box, estr,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, swz, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? NVFP4_OK : NVFP4_ECUDA;
+}
+
+int make_map(CUtensorMap *m, CUtensorMapDataType type, int elem_bytes, const void *base,
+             uint64_t cols, uint64_t rows, uint32_t box_cols, uint32_t box_rows,
+             CUtensorMapSwizzle swz) {
+  return make_map_pitch(m, type, base, cols, rows, cols * elem_bytes, box_cols, box_rows, swz);
 }
 
 int gemm_tile_n() { return BN; }

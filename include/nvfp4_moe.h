@@ -390,6 +390,123 @@ NVFP4_API int moe_nvfp4_forward_w4a4_profiled(
     const uint8_t *w_dn, const uint8_t *sf_dn, const float *g_dn, __nv_bfloat16 *out,
     void *workspace, size_t ws_bytes, void *const *stage_events, cudaStream_t stream);
 
+/* ---------------------------------------------------------------- norms around a block */
+
+/* Root-mean-square norm of rows of H values: n(x) = x / sqrt(mean(x^2) + eps).  Statistics
+ * and sums are fp32; every bf16 result is rounded once from fp32.
+ *   x, y, residual, dy, ...  [T, H] bf16      weight, next_weight, dweight  [H] bf16
+ *   eps      > 0 (an all-zero row gives zeros)
+ *   gate     [gate_rows, gate_cols] bf16 with gate_rows 1 or T and gate_cols 1 or H,
+ *            broadcast over [T, H]; or NULL with gate_rows = gate_cols = 0 for no gate
+ * T == 0 enqueues nothing (a gradient summed over tokens is set to zero).  Outputs must not
+ * overlap inputs or one another.  Infinite or NaN values stay in their own row, except in the
+ * gradients that are summed over rows.
+ * Limits: H % 8 == 0, H <= 32768 (pre_norm_int8: H % 16 == 0).
+ * Alignment: 16 bytes; a gate with gate_cols 1, and its gradient, 2 bytes; scales 4 bytes.
+ * Errors: EINVAL, ESHAPE, EWORKSPACE (backward), ECUDA.
+ *
+ * moe_nvfp4_pre_norm, before a block:          out = weight n(x)
+ * moe_nvfp4_pre_norm_int8, the same handed out as 8-bit rows for nvfp4_int8_matmul: codes
+ * and scales are what nvfp4_int8_quantize gives for the unrounded weight n(x). */
+NVFP4_API int moe_nvfp4_pre_norm(const __nv_bfloat16 *x, const __nv_bfloat16 *weight, int64_t T,
+                                 int64_t H, float eps, __nv_bfloat16 *out, cudaStream_t stream);
+NVFP4_API int moe_nvfp4_pre_norm_int8(const __nv_bfloat16 *x, const __nv_bfloat16 *weight,
+                                      int64_t T, int64_t H, float eps, int8_t *codes,
+                                      float *scales, cudaStream_t stream);
+
+/* After a block, y its output (e.g. of moe_nvfp4_layer) and residual its input:
+ *   out  = residual_scale residual + gate (weight n(y))
+ *   next = next_weight n(out), from the unrounded out: the following block's pre-norm
+ * next_weight and next are both given or both NULL. */
+NVFP4_API int moe_nvfp4_post_norm(const __nv_bfloat16 *y, const __nv_bfloat16 *weight,
+                                  const __nv_bfloat16 *residual, const __nv_bfloat16 *gate,
+                                  int64_t T, int64_t H, int64_t gate_rows, int64_t gate_cols,
+                                  float eps, float residual_scale,
+                                  const __nv_bfloat16 *next_weight, __nv_bfloat16 *out,
+                                  __nv_bfloat16 *next, cudaStream_t stream);
+
+/* Gradients.  With r = 1 / sqrt(mean(x^2) + eps), n = r x:
+ *   pre_norm:   dx = dskip + r (dy weight - n mean(dy weight n)),  dweight = sum_t dy n
+ *               dskip [T, H]: the gradient that reaches x past the block, or NULL for 0
+ *   post_norm:  as above with dout gate in the place of dy;  dresidual = residual_scale dout
+ *               (NULL: not wanted);  dgate = dout weight n summed over the axes along which
+ *               gate is broadcast, [gate_rows, gate_cols] (NULL exactly when gate is)
+ * Sums over tokens are taken in an order that the sizes fix: equal calls on one kind of device
+ * give equal bits.  Workspace: moe_nvfp4_norm_backward_workspace_size bytes, 16-byte aligned,
+ * no initialisation; calls that share one must not overlap in time. */
+NVFP4_API size_t moe_nvfp4_norm_backward_workspace_size(int64_t T, int64_t H);
+NVFP4_API int moe_nvfp4_pre_norm_backward(const __nv_bfloat16 *dy, const __nv_bfloat16 *x,
+                                          const __nv_bfloat16 *weight,
+                                          const __nv_bfloat16 *dskip, int64_t T, int64_t H,
+                                          float eps, __nv_bfloat16 *dx, __nv_bfloat16 *dweight,
+                                          void *workspace, size_t ws_bytes, cudaStream_t stream);
+NVFP4_API int moe_nvfp4_post_norm_backward(
+    const __nv_bfloat16 *dout, const __nv_bfloat16 *y, const __nv_bfloat16 *weight,
+    const __nv_bfloat16 *gate, int64_t T, int64_t H, int64_t gate_rows, int64_t gate_cols,
+    float eps, float residual_scale, __nv_bfloat16 *dy, __nv_bfloat16 *dweight,
+    __nv_bfloat16 *dgate, __nv_bfloat16 *dresidual, void *workspace, size_t ws_bytes,
+    cudaStream_t stream);
+
+/* ---------------------------------------------------------------- gated projection */
+
+#define NVFP4_ACT_SILU 0   /* z / (1 + exp(-z)) */
+#define NVFP4_ACT_GELU 1   /* z / 2 (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) */
+
+/* The gate and up projections of a feed-forward block, the activation and the product in one
+ * kernel, for serving and for training (the first half of moe_nvfp4_shared_expert on its own):
+ *   [g | u] = x w_gu^T          g, u: I columns each, fp32
+ *   h  = bf16( act(g) u )
+ *   gu = bf16( [g | u] )        kept for the gradients when not NULL
+ *   x [T, H] bf16   w_gu [2I, H] bf16 (gate rows, then up rows)   h [T, I] bf16
+ *   gu [T, 2I] bf16 or NULL      act NVFP4_ACT_*
+ * error_flag: [1] int32, device, may be NULL: bit 1 is ORed in if a device-side wait gave up
+ * (the outputs are then invalid); nothing else is written, so the caller zeroes it once.
+ * No workspace.  T == 0 enqueues nothing.
+ * Limits: H % 8 == 0, I % 8 == 0, H and I <= 65536, T < 2^30.  Alignment: 16 bytes
+ * (error_flag 4).  Outputs must not overlap inputs.  Errors: EINVAL, ESHAPE, ECUDA. */
+NVFP4_API int moe_nvfp4_gate_up(const __nv_bfloat16 *x, const __nv_bfloat16 *w_gu, int64_t T,
+                                int64_t H, int64_t I, int act, __nv_bfloat16 *h,
+                                __nv_bfloat16 *gu, int32_t *error_flag, cudaStream_t stream);
+
+/* Its gradients from dh [T, I] and the kept gu:
+ *   dg = bf16( dh u act'(g) ),  du = bf16( dh act(g) )      into the workspace
+ *   dx    = bf16( [dg | du] w_gu )      [T, H], or NULL: not wanted (w_gu may then be NULL)
+ *   dw_gu = bf16( [dg | du]^T x )       [2I, H], or NULL: not wanted (x may then be NULL)
+ * with fp32 sums whose order the sizes fix.  T == 0 sets dw_gu to zero.
+ * Workspace: moe_nvfp4_gate_up_backward_workspace_size bytes, 16-byte aligned, no
+ * initialisation.  Limits, alignment and error_flag as moe_nvfp4_gate_up.
+ * Errors: EINVAL (also dx and dw_gu both NULL), ESHAPE, EWORKSPACE, ECUDA. */
+NVFP4_API size_t moe_nvfp4_gate_up_backward_workspace_size(int64_t T, int64_t I);
+NVFP4_API int moe_nvfp4_gate_up_backward(const __nv_bfloat16 *dh, const __nv_bfloat16 *x,
+                                         const __nv_bfloat16 *w_gu, const __nv_bfloat16 *gu,
+                                         int64_t T, int64_t H, int64_t I, int act,
+                                         __nv_bfloat16 *dx, __nv_bfloat16 *dw_gu,
+                                         void *workspace, size_t ws_bytes, int32_t *error_flag,
+                                         cudaStream_t stream);
+
+/* ---------------------------------------------------------------- 8-bit integers */
+
+/* Rows of bf16 to signed 8-bit codes and one scale each (activations: a row is a token;
+ * weights: a row is an output channel), symmetric:
+ *   amax = max |x| of the row;  scale = amax / 127 (1 for an all-zero row)
+ *   code = the integer nearest to 127 x / amax, ties to even (0 for an all-zero row)
+ * The quotient is rounded as the real one would be, so codes are exact.  A row with NaN or
+ * infinite values gets unspecified codes; other rows are not touched by it.
+ *   x [rows, cols] bf16    codes [rows, cols] int8    scales [rows] fp32
+ * rows == 0 enqueues nothing.  Limits: cols % 16 == 0, cols <= 32768.  Alignment: x and codes
+ * 16 bytes, scales 4.  Errors: EINVAL, ESHAPE, ECUDA. */
+NVFP4_API int nvfp4_int8_quantize(const __nv_bfloat16 *x, int64_t rows, int64_t cols,
+                                  int8_t *codes, float *scales, cudaStream_t stream);
+
+/* out[t, n] = bf16( (sum_k a[t, k] w[n, k]) a_scales[t] w_scales[n] ): exact int32 sums.
+ *   a [T, K] int8   a_scales [T] fp32   w [N, K] int8   w_scales [N] fp32   out [T, N] bf16
+ * error_flag as in moe_nvfp4_gate_up.  No workspace.  T == 0 enqueues nothing.
+ * Limits: K % 16 == 0, K <= 32768, N % 8 == 0, N <= 2^24, T < 2^30.  Alignment: a, w,
+ * w_scales and out 16 bytes, a_scales and error_flag 4.  Errors: EINVAL, ESHAPE, ECUDA. */
+NVFP4_API int nvfp4_int8_matmul(const int8_t *a, const float *a_scales, const int8_t *w,
+                                const float *w_scales, int64_t T, int64_t N, int64_t K,
+                                __nv_bfloat16 *out, int32_t *error_flag, cudaStream_t stream);
+
 /* ---------------------------------------------------------------- fixed-scratch forward */
 
 /* Bytes of the fixed scratch of moe_nvfp4_forward_static: it holds 256 bytes of counters,

@@ -1,0 +1,220 @@
+"""The gated projection and its gradients against plain 64-bit formulas.
+
+Tolerances: products of bf16 values are exact; a tensor-core sum of K of them is taken to be
+off by at most K 2^-23 of the sum of their magnitudes (one fp32 step a term, also where the
+hardware truncates).  Activations and their slopes are off by less than 2^-19 (1 + |z|); the
+slopes lie within [-0.13, 1.13].  Each bf16 rounding is 2^-8 relative: the result's own, and in
+the gradients that of dg and du, whose terms' magnitudes bound its effect on each element; as
+rounding errors of one sum are independent of each other, the whole result (2-norm) has to be
+within 2^-8 too: two roundings of at most 2^-8 / sqrt(3) rms each."""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+B, U = 2.0 ** -8, 2.0 ** -23
+
+
+@pytest.fixture(scope="module")
+def nv():
+    import bit_quantized_moe_nvfp4_b200 as m
+    return m
+
+
+def draw(seed, *shape, std=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(shape, generator=g) * std).to(torch.bfloat16)
+
+
+def act_fn(act, z):
+    if act == 0:
+        return z * torch.sigmoid(z)
+    return 0.5 * z * (1 + torch.tanh((2 / torch.pi) ** 0.5 * (z + 0.044715 * z ** 3)))
+
+
+def close(got, ref, slack):
+    g = got.detach().cpu().double()
+    ref, slack = ref.cpu(), slack.cpu()
+    assert g.shape == ref.shape
+    bad = (g - ref).abs() > B * ref.abs() + slack
+    assert not bad.any(), (int(bad.sum()), float((g - ref).abs().max()), bad.nonzero()[:4])
+
+
+def near(got, ref):
+    d = torch.linalg.vector_norm(got.detach().double().cpu() - ref.cpu())
+    n = torch.linalg.vector_norm(ref.cpu())
+    assert d <= B * n, float(d / n)
+
+
+def inputs(T, H, I):
+    return draw(T + H, T, H), draw(I + H, 2 * I, H, std=H ** -0.5)
+
+
+# T up to 16, 32, 64, 128 and above: each column tile of the split kernel; many rows and
+# columns: pairs of CTAs.  Sizes that end inside every tile.
+SHAPES = [(1, 64, 8), (2, 200, 72), (16, 264, 64), (17, 136, 200), (33, 64, 136), (64, 512, 64),
+          (65, 72, 328), (129, 264, 520), (300, 128, 8), (257, 192, 2056), (1000, 520, 1032),
+          (2049, 64, 1024)]
+
+
+@pytest.mark.parametrize("T,H,I", SHAPES)
+@pytest.mark.parametrize("act", [0, 1], ids=["silu", "gelu"])
+def test_gate_up(nv, T, H, I, act):
+    x, w = inputs(T, H, I)
+    gu = torch.full((T, 2 * I), float("nan"), dtype=torch.bfloat16, device="cuda")
+    flag = torch.zeros(1, dtype=torch.int32, device="cuda")
+    h = nv.moe_nvfp4_gate_up(x.cuda(), w.cuda(), act=act, gu=gu, error_flag=flag)
+    alone = nv.moe_nvfp4_gate_up(x.cuda(), w.cuda(), act=act)
+    assert int(flag) == 0
+    assert torch.equal(h, alone)
+    xd, wd = x.cuda().double(), w.cuda().double()
+    ref = xd @ wd.t()
+    mag = (xd.abs() @ wd.abs().t()) * (H * U)
+    close(gu, ref, mag)
+    g, u, eg, eu = ref[:, :I], ref[:, I:], mag[:, :I], mag[:, I:]
+    a = act_fn(act, g)
+    ea = 1.13 * eg + 2.0 ** -19 * (1 + g.abs())
+    close(h, a * u, ea * u.abs() + a.abs() * eu + ea * eu)
+
+
+def dgu_ref(gu, dh, act):
+    gu = gu.double().requires_grad_()
+    I = gu.shape[1] // 2
+    d, = torch.autograd.grad(act_fn(act, gu[:, :I]) * gu[:, I:], gu, dh.double())
+    return d
+
+
+@pytest.mark.parametrize("T,H,I", SHAPES + [(4096, 256, 64), (40, 2048, 1032)])
+@pytest.mark.parametrize("act", [0, 1], ids=["silu", "gelu"])
+def test_gate_up_backward(nv, T, H, I, act):
+    x, w = (t.cuda() for t in inputs(T, H, I))
+    gu, dh = draw(3, T, 2 * I, std=1.5).cuda(), draw(4, T, I, std=0.1).cuda()
+    flag = torch.zeros(1, dtype=torch.int32, device="cuda")
+    dx, dw = nv.moe_nvfp4_gate_up_backward(dh, x, w, gu, act=act, error_flag=flag)
+    one = nv.moe_nvfp4_gate_up_backward(dh, x, w, gu, act=act, need_dw=False)
+    two = nv.moe_nvfp4_gate_up_backward(dh, x, w, gu, act=act, need_dx=False)
+    assert int(flag) == 0
+    assert one[1] is None and two[0] is None
+    assert torch.equal(one[0], dx) and torch.equal(two[1], dw)   # one order of summation
+    d = dgu_ref(gu, dh, act)
+    # terms of d whose error is not relative to d itself: 2^-19 (1 + |z|) |dh| (1 + |u|)
+    ed = 2.0 ** -19 * (1 + gu.double().abs()) * dh.double().abs().repeat(1, 2) * \
+        (1 + gu.double().abs().roll(I, 1))
+    xd, wd = x.double(), w.double()
+    for got, ref, m in ((dx, d @ wd, lambda t: t @ wd.abs()),
+                        (dw, d.t() @ xd, lambda t: t.t() @ xd.abs())):
+        K = 2 * I if got is dx else T
+        close(got, ref, m(d.abs()) * (B + K * U) + m(ed))
+        near(got, ref)
+
+
+def test_gradients_against_differences(nv):
+    T, H, I, h = 5, 72, 40, 1e-5
+    x, w = inputs(T, H, I)
+    dh = draw(9, T, I)
+    gu = torch.empty(T, 2 * I, dtype=torch.bfloat16, device="cuda")
+    nv.moe_nvfp4_gate_up(x.cuda(), w.cuda(), gu=gu)
+    got = nv.moe_nvfp4_gate_up_backward(dh.cuda(), x.cuda(), w.cuda(), gu)
+
+    def f(x, w):
+        z = x @ w.t()
+        return float((act_fn(0, z[:, :I]) * z[:, I:] * dh.double()).sum())
+
+    xd, wd = x.double(), w.double()
+    d = dgu_ref((xd @ wd.t()), dh, 0).abs()
+    # dg and du: rounded once, from g and u that were rounded once (slopes up to 1.13, second
+    # derivatives up to 0.8): 4 roundings of their terms bound both
+    mags = ((d + dh.double().abs().repeat(1, 2)) @ wd.abs(),
+            (d + dh.double().abs().repeat(1, 2)).t() @ xd.abs())
+    for k in range(2):
+        e = torch.randn((xd, wd)[k].shape, generator=torch.Generator().manual_seed(k),
+                        dtype=torch.float64)
+        a = (xd + h * e, wd) if k == 0 else (xd, wd + h * e)
+        b = (xd - h * e, wd) if k == 0 else (xd, wd - h * e)
+        diff = (f(*a) - f(*b)) / (2 * h)
+        tol = float((mags[k] * e.abs()).sum()) * 4 * B + 1e-3
+        assert abs(diff - float((got[k].cpu().double() * e).sum())) <= tol
+
+
+def test_large_and_special_pre_activations(nv):
+    """|z| far beyond exp's range, zeros, and infinities: what the formulas give."""
+    I, H = 8, 8
+    z = torch.tensor([-200.0, -90.0, -20.0, 0.0, 20.0, 90.0, 200.0, 1e4]).bfloat16()
+    x = torch.zeros(1, H, dtype=torch.bfloat16)
+    x[0, 0] = 1
+    w = torch.zeros(2 * I, H, dtype=torch.bfloat16)
+    w[:I, 0], w[I:, 0] = z, 1
+    for act in (0, 1):
+        h = nv.moe_nvfp4_gate_up(x.cuda(), w.cuda(), act=act).cpu().double()[0]
+        ref = act_fn(act, z.double())
+        assert ((h - ref).abs() <= B * ref.abs() + 2.0 ** -19 * (1 + z.double().abs())).all()
+        gu = torch.cat([z, torch.ones(I).bfloat16()]).unsqueeze(0).cuda()
+        dh = torch.ones(1, I, dtype=torch.bfloat16).cuda()
+        _, dw = nv.moe_nvfp4_gate_up_backward(dh, x.cuda(), w.cuda(), gu, act=act)
+        assert dw.isfinite().all()
+        assert (dw[:I, 0].cpu().double() - dgu_ref(gu.cpu(), dh.cpu(), act)[0, :I]).abs().max() \
+            <= 2 * B
+
+
+def test_rows_of_nan_stay_their_own(nv):
+    for T in (5, 40, 700):
+        x, w = inputs(T, 136, 520)
+        bad = x.clone()
+        bad[2] = float("nan")
+        a = nv.moe_nvfp4_gate_up(x.cuda(), w.cuda())
+        b = nv.moe_nvfp4_gate_up(bad.cuda(), w.cuda())
+        keep = torch.arange(T) != 2
+        assert torch.equal(a.cpu()[keep], b.cpu()[keep])
+        assert b[2].isnan().all()
+
+
+def test_outputs_end_where_they_end(nv):
+    """Rows behind the last token and the bytes around a result stay as they were."""
+    for T, H, I in ((5, 136, 72), (300, 136, 1032)):
+        x, w = inputs(T, H, I)
+        buf = torch.full((T + 8, I), 7.0, dtype=torch.bfloat16, device="cuda")
+        gbuf = torch.full((T + 8, 2 * I), 7.0, dtype=torch.bfloat16, device="cuda")
+        nv.moe_nvfp4_gate_up(x.cuda(), w.cuda(), h=buf[:T], gu=gbuf[:T])
+        assert (buf[T:] == 7).all() and (gbuf[T:] == 7).all()
+        dxb = torch.full((T + 8, H), 7.0, dtype=torch.bfloat16, device="cuda")
+        dwb = torch.full((2 * I + 8, H), 7.0, dtype=torch.bfloat16, device="cuda")
+        nv.moe_nvfp4_gate_up_backward(buf[:T], x.cuda(), w.cuda(), gbuf[:T], dx=dxb[:T],
+                                      dw_gu=dwb[:2 * I])
+        assert (dxb[T:] == 7).all() and (dwb[2 * I:] == 7).all()
+
+
+def test_zero_tokens(nv):
+    x, w = torch.empty(0, 64, dtype=torch.bfloat16).cuda(), draw(1, 32, 64).cuda()
+    h = nv.moe_nvfp4_gate_up(x, w)
+    assert h.shape == (0, 16)
+    gu = torch.empty(0, 32, dtype=torch.bfloat16).cuda()
+    dx, dw = nv.moe_nvfp4_gate_up_backward(h, x, w, gu, dw_gu=torch.ones_like(w))
+    assert dx.shape == (0, 64) and (dw == 0).all()
+
+
+def test_another_stream_and_a_graph(nv):
+    for T in (8, 600):
+        x, w = (t.cuda() for t in inputs(T, 256, 1024))
+        dh = draw(5, T, 1024).cuda()
+
+        def step(x):
+            gu = torch.empty(T, 2048, dtype=torch.bfloat16, device="cuda")
+            h = nv.moe_nvfp4_gate_up(x, w, gu=gu)
+            return (h,) + nv.moe_nvfp4_gate_up_backward(dh, x, w, gu)
+
+        want = step(x)
+        torch.cuda.synchronize()
+        s, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            a = step(x)
+        with torch.cuda.stream(s2):   # two calls at once
+            b = step(x)
+        torch.cuda.synchronize()
+        xin = torch.zeros_like(x)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            c = step(xin)
+        xin.copy_(x)
+        g.replay()
+        torch.cuda.synchronize()
+        for got in (a, b, c):
+            assert all(torch.equal(p, q) for p, q in zip(got, want))

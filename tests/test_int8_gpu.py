@@ -1,0 +1,134 @@
+"""The product of 8-bit integers against exact integer sums, and the operators around a block
+run together.
+
+Sums are exact, so out differs from the real value by two fp32 products, the sum's conversion
+to fp32 (2^-24 each) and one rounding to bf16: (2^-8 + 2^-22) |out|."""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+B = 2.0 ** -8
+EPS = 1e-5
+
+
+@pytest.fixture(scope="module")
+def nv():
+    import bit_quantized_moe_nvfp4_b200 as m
+    return m
+
+
+def case(T, N, K, seed=0, full=False):
+    g = torch.Generator().manual_seed(seed + T + N + K)
+    lo, hi = (-127, 128)
+    a = torch.randint(lo, hi, (T, K), generator=g, dtype=torch.int8)
+    w = torch.randint(lo, hi, (N, K), generator=g, dtype=torch.int8)
+    if full:
+        a[:], w[:] = 127, 127
+        w[::2] = -127
+    return a, torch.rand(T, generator=g) + 0.1, w, torch.rand(N, generator=g) * 1e-3 + 1e-5
+
+
+SHAPES = [(1, 8, 16), (1, 1000, 784), (2, 72, 2064), (16, 136, 128), (17, 264, 400), (33, 64, 128),
+          (65, 328, 272), (129, 1000, 528), (300, 8, 16), (257, 2056, 336), (1000, 2064, 1040),
+          (2049, 1032, 64), (4, 256, 32768)]
+
+
+@pytest.mark.parametrize("T,N,K", SHAPES)
+@pytest.mark.parametrize("full", [False, True], ids=["random", "extreme"])
+def test_int8_matmul(nv, T, N, K, full):
+    a, sa, w, sw = case(T, N, K, full=full)
+    flag = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = nv.nvfp4_int8_matmul(a.cuda(), sa.cuda(), w.cuda(), sw.cuda(), error_flag=flag)
+    assert int(flag) == 0
+    acc = (a.cuda().double() @ w.cuda().double().t()).cpu()
+    ref = acc * sa.double()[:, None] * sw.double()
+    assert ((out.cpu().double() - ref).abs() <= (B + 2.0 ** -22) * ref.abs()).all()
+
+
+def test_int8_matmul_of_minus_128(nv):
+    """Codes of -128, which the quantizer never gives, are taken as they are."""
+    a = torch.full((3, 64), -128, dtype=torch.int8)
+    out = nv.nvfp4_int8_matmul(a.cuda(), torch.ones(3).cuda(), a[:1].repeat(8, 1).cuda(),
+                               torch.ones(8).cuda())
+    assert (out == 128 * 128 * 64).all()
+
+
+def test_both_kernels_agree_on_rows(nv):
+    """A token's result does not depend on how many tokens come with it."""
+    a, sa, w, sw = (t.cuda() for t in case(2300, 2048, 512))
+    whole = nv.nvfp4_int8_matmul(a, sa, w, sw)
+    for n in (1, 9, 40, 100, 130):
+        assert torch.equal(nv.nvfp4_int8_matmul(a[:n], sa[:n], w, sw), whole[:n])
+
+
+def test_output_ends_where_it_ends(nv):
+    for T, N in ((5, 72), (300, 2056)):
+        a, sa, w, sw = (t.cuda() for t in case(T, N, 144))
+        buf = torch.full((T + 8, N), 7.0, dtype=torch.bfloat16, device="cuda")
+        nv.nvfp4_int8_matmul(a, sa, w, sw, out=buf[:T])
+        assert (buf[T:] == 7).all()
+
+
+def test_zero_tokens(nv):
+    _, _, w, sw = case(1, 64, 64)
+    out = nv.nvfp4_int8_matmul(torch.empty(0, 64, dtype=torch.int8).cuda(),
+                               torch.empty(0).cuda(), w.cuda(), sw.cuda())
+    assert out.shape == (0, 64)
+
+
+def test_other_streams_and_a_graph(nv):
+    for T in (7, 700):
+        a, sa, w, sw = (t.cuda() for t in case(T, 2048, 768))
+        want = nv.nvfp4_int8_matmul(a, sa, w, sw)
+        torch.cuda.synchronize()
+        outs = []
+        for _ in range(2):
+            with torch.cuda.stream(torch.cuda.Stream()):
+                outs.append(nv.nvfp4_int8_matmul(a, sa, w, sw))
+        ain = torch.zeros_like(a)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(nv.nvfp4_int8_matmul(ain, sa, w, sw))
+        ain.copy_(a)
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, want) for o in outs)
+
+
+@pytest.mark.parametrize("T", [1, 40, 700])
+def test_a_block_between_its_norms(nv, T):
+    """pre-norm -> gated projection (bf16) -> 8-bit down projection -> post-norm with a gate
+    and the next pre-norm, as a decoder layer runs them, against 64 bits.
+
+    2-norm bound: roundings of the normed rows, of h and of the block's output (2^-8 each, two
+    factors h = act(g) u of the first), the 8-bit step of h's rows, and the result's."""
+    H, I = 512, 1024
+    gen = torch.Generator().manual_seed(T)
+    r = lambda *s, std=1.0, mean=0.0: (torch.randn(s, generator=gen) * std + mean).bfloat16()
+    x, w1, w2, w3 = r(T, H), r(H, std=0.1, mean=1.0), r(H, std=0.1, mean=1.0), r(H, std=0.1, mean=1.0)
+    w_gu, gate = r(2 * I, H, std=H ** -0.5), r(1, H, std=0.1, mean=0.5)
+    w_dn = r(H, I, std=I ** -0.5)
+    wq, ws = nv.nvfp4_int8_quantize(w_dn.cuda())
+    n1 = nv.moe_nvfp4_pre_norm(x.cuda(), w1.cuda(), EPS)
+    h = nv.moe_nvfp4_gate_up(n1, w_gu.cuda())
+    y = nv.nvfp4_int8_matmul(*nv.nvfp4_int8_quantize(h), wq, ws)
+    out, nxt = nv.moe_nvfp4_post_norm(y, w2.cuda(), x.cuda(), EPS, gate=gate.cuda(),
+                                      residual_scale=0.5, next_weight=w3.cuda())
+    q, s = nv.moe_nvfp4_pre_norm_int8(x.cuda(), w1.cuda(), EPS)
+    d = lambda t: t.double()
+    norm = lambda t: t * torch.rsqrt((t * t).mean(-1, keepdim=True) + EPS)
+    n1d = norm(d(x)) * d(w1)
+    z = n1d @ d(w_gu).t()
+    hd = z[:, :I] * torch.sigmoid(z[:, :I]) * z[:, I:]
+    yd = hd @ (wq.cpu().double() * ws.cpu().double()[:, None]).t()
+    od = 0.5 * d(x) + d(gate) * (norm(yd) * d(w2))
+    nd = norm(od) * d(w3)
+    step = hd.abs().amax(-1, keepdim=True) / 127 / 12 ** 0.5     # rms of the rounding to codes
+    rel8 = float((step * I ** 0.5).norm() / hd.norm())
+    bound = 6 * B + 1.5 * rel8
+    for got, ref in ((out, od), (nxt, nd)):
+        err = float((got.cpu().double() - ref).norm() / ref.norm())
+        assert err <= bound, (err, bound)
+    deq = q.cpu().double() * s.cpu().double()[:, None]
+    assert ((deq - n1d).abs() <= 0.51 * s.cpu().double()[:, None]).all()
