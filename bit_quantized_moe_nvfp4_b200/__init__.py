@@ -568,58 +568,65 @@ def moe_nvfp4_forward_static(x, topk_ids, topk_w, w_gu, s_gu, g_gu, w_dn, s_dn, 
 
 
 # ------------------------------------------------------------------------------ dense operators
-def _arg(t, dtype, shape, device, name: str, optional: bool = False):
-    """Address of a contiguous CUDA tensor of this type, shape and device (None: no tensor,
-    where that is allowed)."""
-    if t is None and optional:
-        return None
-    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.device != device \
-            or tuple(t.shape) != shape or not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {shape} "
-                         f"on {device if device.type == 'cuda' else 'a CUDA device'}")
-    return t.data_ptr()
+# One token's call is shorter on the GPU than in Python, so these helpers do little: the raw
+# stream handle instead of a Stream object (2 us less a call), one attribute test each.
+def _arg(t, dtype, shape, dev: int, name: str):
+    """Address of a contiguous tensor of this type and shape on CUDA device `dev`."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == dev >= 0 \
+                and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on "
+                     + (f"cuda:{dev}" if dev >= 0 else "a CUDA device"))
+
+
+def _optional(t, dtype, shape, dev: int, name: str):
+    return None if t is None else _arg(t, dtype, shape, dev, name)
+
+
+def _out(t, like, dtype, shape, dev: int, name: str):
+    """(`t`, or a new tensor beside `like`; its address)."""
+    if t is None:
+        t = torch.empty(*shape, dtype=dtype, device=like.device)
+        return t, t.data_ptr()
+    return t, _arg(t, dtype, shape, dev, name)
 
 
 def _rows(x, name: str):
-    """(T, H, device) of a two-dimensional tensor."""
+    """(T, H, device index) of a two-dimensional tensor."""
     if not isinstance(x, torch.Tensor) or x.dim() != 2:
         raise ValueError(f"{name}: expected a two-dimensional tensor")
-    return x.shape[0], x.shape[1], x.device
+    T, H = x.shape
+    return T, H, x.get_device()
 
 
-def _new(out, shape, dtype, device, name: str):
-    """(`out` or a new tensor, its address)."""
-    if out is None:
-        out = torch.empty(shape, dtype=dtype, device=device)
-        return out, out.data_ptr()
-    return out, _arg(out, dtype, shape, device, name)
-
-
-def _scratch(workspace, nbytes: int, device):
-    """(workspace, its address, its bytes), allocated when none is given."""
+def _scratch(workspace, nbytes: int, like):
+    """(workspace, its address, its bytes), allocated beside `like` when none is given."""
     if workspace is None:
-        workspace = torch.empty((max(nbytes, 16),), dtype=torch.uint8, device=device)
-    elif not isinstance(workspace, torch.Tensor) or workspace.dtype is not torch.uint8 \
-            or workspace.device != device or not workspace.is_contiguous():
-        raise ValueError(f"workspace: expected a contiguous torch.uint8 tensor on {device}")
+        workspace = like.new_empty((nbytes,), dtype=torch.uint8)
+    elif workspace.dtype is not torch.uint8 or workspace.get_device() != like.get_device() \
+            or not workspace.is_contiguous():
+        raise ValueError("workspace: expected a contiguous torch.uint8 tensor on the inputs' "
+                         "device")
     return workspace, workspace.data_ptr(), workspace.numel()
 
 
-def _run(name: str, device, *args) -> None:
-    """Call an entry point on the tensors' device and that device's current stream."""
-    f = getattr(_lib(), name)
-    stream = torch.cuda.current_stream(device).cuda_stream
-    if device.index == torch.cuda.current_device():
-        status = f(*args, stream)
+def _run(name: str, dev: int, *args) -> None:
+    """Call an entry point on CUDA device `dev` and that device's current stream."""
+    f = getattr(_LIB or _lib(), name)
+    if dev == torch._C._cuda_getDevice():
+        status = f(*args, torch._C._cuda_getCurrentRawStream(dev))
     else:
-        with torch.cuda.device(device):
-            status = f(*args, stream)
+        with torch.cuda.device(dev):
+            status = f(*args, torch._C._cuda_getCurrentRawStream(dev))
     if status:
         _check(status)
 
 
-def _flag(error_flag, device):
-    return _arg(error_flag, torch.int32, (1,), device, "error_flag", optional=True)
+def _flag(error_flag, dev: int):
+    return None if error_flag is None else _arg(error_flag, torch.int32, (1,), dev, "error_flag")
 
 
 def moe_nvfp4_pre_norm(x, weight, eps: float, out=None) -> torch.Tensor:
@@ -627,7 +634,7 @@ def moe_nvfp4_pre_norm(x, weight, eps: float, out=None) -> torch.Tensor:
     T, H, dev = _rows(x, "x")
     px = _arg(x, torch.bfloat16, (T, H), dev, "x")
     pw = _arg(weight, torch.bfloat16, (H,), dev, "weight")
-    out, po = _new(out, (T, H), torch.bfloat16, dev, "out")
+    out, po = _out(out, x, torch.bfloat16, (T, H), dev, "out")
     _run("moe_nvfp4_pre_norm", dev, px, pw, T, H, eps, po)
     return out
 
@@ -638,8 +645,8 @@ def moe_nvfp4_pre_norm_int8(x, weight, eps: float, codes=None, scales=None):
     T, H, dev = _rows(x, "x")
     px = _arg(x, torch.bfloat16, (T, H), dev, "x")
     pw = _arg(weight, torch.bfloat16, (H,), dev, "weight")
-    codes, pc = _new(codes, (T, H), torch.int8, dev, "codes")
-    scales, ps = _new(scales, (T,), torch.float32, dev, "scales")
+    codes, pc = _out(codes, x, torch.int8, (T, H), dev, "codes")
+    scales, ps = _out(scales, x, torch.float32, (T,), dev, "scales")
     _run("moe_nvfp4_pre_norm_int8", dev, px, pw, T, H, eps, pc, ps)
     return codes, scales
 
@@ -664,13 +671,13 @@ def moe_nvfp4_post_norm(y, weight, residual, eps: float, gate=None, residual_sca
     pw = _arg(weight, bf, (H,), dev, "weight")
     pr = _arg(residual, bf, (T, H), dev, "residual")
     pg, rows, cols = _gate(gate, T, H, dev)
-    pn = _arg(next_weight, bf, (H,), dev, "next_weight", optional=True)
+    pn = _optional(next_weight, bf, (H,), dev, "next_weight")
     if pn is None and next_out is not None:
         raise ValueError("next_out needs next_weight")
-    out, po = _new(out, (T, H), bf, dev, "out")
+    out, po = _out(out, y, bf, (T, H), dev, "out")
     po2 = None
     if pn is not None:
-        next_out, po2 = _new(next_out, (T, H), bf, dev, "next_out")
+        next_out, po2 = _out(next_out, y, bf, (T, H), dev, "next_out")
     _run("moe_nvfp4_post_norm", dev, py, pw, pr, pg, T, H, rows, cols, eps, residual_scale, pn,
          po, po2)
     return out if pn is None else (out, next_out)
@@ -689,16 +696,16 @@ def moe_nvfp4_pre_norm_backward(dy, x, weight, eps: float, dskip=None, dx=None, 
     pd = _arg(dy, bf, (T, H), dev, "dy")
     px = _arg(x, bf, (T, H), dev, "x")
     pw = _arg(weight, bf, (H,), dev, "weight")
-    ps = _arg(dskip, bf, (T, H), dev, "dskip", optional=True)
-    dx, pdx = _new(dx, (T, H), bf, dev, "dx")
-    dweight, pdw = _new(dweight, (H,), bf, dev, "dweight")
-    workspace, pws, nws = _scratch(workspace, _norm_scratch(T, H, dev), dev)
+    ps = _optional(dskip, bf, (T, H), dev, "dskip")
+    dx, pdx = _out(dx, x, bf, (T, H), dev, "dx")
+    dweight, pdw = _out(dweight, x, bf, (H,), dev, "dweight")
+    workspace, pws, nws = _scratch(workspace, _norm_scratch(T, H, dev), x)
     _run("moe_nvfp4_pre_norm_backward", dev, pd, px, pw, ps, T, H, eps, pdx, pdw, pws, nws)
     return dx, dweight
 
 
 def _norm_scratch(T, H, dev):
-    if dev.index == torch.cuda.current_device():
+    if dev == torch._C._cuda_getDevice():
         return _lib().moe_nvfp4_norm_backward_workspace_size(T, H)
     with torch.cuda.device(dev):
         return _lib().moe_nvfp4_norm_backward_workspace_size(T, H)
@@ -716,16 +723,16 @@ def moe_nvfp4_post_norm_backward(dout, y, weight, eps: float, gate=None,
     py = _arg(y, bf, (T, H), dev, "y")
     pw = _arg(weight, bf, (H,), dev, "weight")
     pg, rows, cols = _gate(gate, T, H, dev)
-    dy, pdy = _new(dy, (T, H), bf, dev, "dy")
-    dweight, pdw = _new(dweight, (H,), bf, dev, "dweight")
+    dy, pdy = _out(dy, y, bf, (T, H), dev, "dy")
+    dweight, pdw = _out(dweight, y, bf, (H,), dev, "dweight")
     pdg = pdr = None
     if gate is not None:
-        dgate, pdg = _new(dgate, (rows, cols), bf, dev, "dgate")
+        dgate, pdg = _out(dgate, y, bf, (rows, cols), dev, "dgate")
     elif dgate is not None:
         raise ValueError("dgate needs gate")
     if need_dresidual or dresidual is not None:
-        dresidual, pdr = _new(dresidual, (T, H), bf, dev, "dresidual")
-    workspace, pws, nws = _scratch(workspace, _norm_scratch(T, H, dev), dev)
+        dresidual, pdr = _out(dresidual, y, bf, (T, H), dev, "dresidual")
+    workspace, pws, nws = _scratch(workspace, _norm_scratch(T, H, dev), y)
     _run("moe_nvfp4_post_norm_backward", dev, pd, py, pw, pg, T, H, rows, cols, eps,
          residual_scale, pdy, pdw, pdg, pdr, pws, nws)
     return dy, dweight, dgate, dresidual
@@ -741,8 +748,8 @@ def moe_nvfp4_gate_up(x, w_gu, act: int = ACT_SILU, h=None, gu=None,
     I = _rows(w_gu, "w_gu")[0] // 2
     px = _arg(x, bf, (T, H), dev, "x")
     pw = _arg(w_gu, bf, (2 * I, H), dev, "w_gu")
-    h, ph = _new(h, (T, I), bf, dev, "h")
-    pgu = _arg(gu, bf, (T, 2 * I), dev, "gu", optional=True)
+    h, ph = _out(h, x, bf, (T, I), dev, "h")
+    pgu = _optional(gu, bf, (T, 2 * I), dev, "gu")
     _run("moe_nvfp4_gate_up", dev, px, pw, T, H, I, act, ph, pgu, _flag(error_flag, dev))
     return h
 
@@ -765,10 +772,10 @@ def moe_nvfp4_gate_up_backward(dh, x, w_gu, gu, act: int = ACT_SILU, dx=None, dw
     pgu = _arg(gu, bf, (T, 2 * I), dev, "gu")
     pdx = pdw = None
     if need_dx or dx is not None:
-        dx, pdx = _new(dx, (T, H), bf, dev, "dx")
+        dx, pdx = _out(dx, x, bf, (T, H), dev, "dx")
     if need_dw or dw_gu is not None:
-        dw_gu, pdw = _new(dw_gu, (2 * I, H), bf, dev, "dw_gu")
-    workspace, pws, nws = _scratch(workspace, 4 * T * I + 256, dev)
+        dw_gu, pdw = _out(dw_gu, x, bf, (2 * I, H), dev, "dw_gu")
+    workspace, pws, nws = _scratch(workspace, moe_nvfp4_gate_up_backward_workspace_size(T, I), x)
     _run("moe_nvfp4_gate_up_backward", dev, pd, px, pw, pgu, T, H, I, act, pdx, pdw, pws, nws,
          _flag(error_flag, dev))
     return dx, dw_gu
@@ -779,8 +786,8 @@ def nvfp4_int8_quantize(x, codes=None, scales=None):
     scale = max |x| / 127, code = the integer nearest to x / scale."""
     T, K, dev = _rows(x, "x")
     px = _arg(x, torch.bfloat16, (T, K), dev, "x")
-    codes, pc = _new(codes, (T, K), torch.int8, dev, "codes")
-    scales, ps = _new(scales, (T,), torch.float32, dev, "scales")
+    codes, pc = _out(codes, x, torch.int8, (T, K), dev, "codes")
+    scales, ps = _out(scales, x, torch.float32, (T,), dev, "scales")
     _run("nvfp4_int8_quantize", dev, px, T, K, pc, ps)
     return codes, scales
 
@@ -794,7 +801,7 @@ def nvfp4_int8_matmul(a, a_scales, w, w_scales, out=None, error_flag=None) -> to
     pw = _arg(w, torch.int8, (N, K), dev, "w")
     pas = _arg(a_scales, torch.float32, (T,), dev, "a_scales")
     pws = _arg(w_scales, torch.float32, (N,), dev, "w_scales")
-    out, po = _new(out, (T, N), torch.bfloat16, dev, "out")
+    out, po = _out(out, a, torch.bfloat16, (T, N), dev, "out")
     _run("nvfp4_int8_matmul", dev, pa, pas, pw, pws, T, N, K, po, _flag(error_flag, dev))
     return out
 

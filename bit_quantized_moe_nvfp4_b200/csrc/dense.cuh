@@ -336,7 +336,7 @@ __device__ __forceinline__ float2 ld_cluster_f2(uint32_t addr) {
 }
 
 template <int KIND, bool AMN, bool BMN, int EPI, int ACT, int NT>
-__global__ void __launch_bounds__(kSThreads)
+__global__ void __launch_bounds__(kSThreads, 2)
     dense_split_kernel(const __grid_constant__ CUtensorMap map_a,
                        const __grid_constant__ CUtensorMap map_b, DenseArgs p) {
   using S = SplitShape<NT>;

@@ -10,10 +10,13 @@
 // With x in registers, mean(dn n) = r sum(dn x) / H, so both sums of a row come from one
 // pass over it and are reduced together.
 //
-// Every kernel here is bound by HBM: a row is read once into registers (16-byte loads) and
-// each output is written once.  A row of at most 1024 values belongs to a warp (no barrier);
-// a longer one to a CTA.  All statistics and sums are fp32; each result is rounded once.
-// next is taken from the unrounded out, and codes from the unrounded y.
+// Every kernel here is bound by HBM: a row is read once and each output written once.  A row
+// of at most 1536 values belongs to a warp (no barrier); a longer one to a CTA.  CTAs are
+// persistent.  Each thread copies the 16-byte vectors that it will itself need of its next
+// rows into shared memory (cp.async), a few rows ahead, so loads stay in flight through the
+// reductions and stores of the present row, without registers or barriers for it.
+// All statistics and sums are fp32; each result is rounded once.  next is taken from the
+// unrounded out, and codes from the unrounded y.
 #include <algorithm>
 #include <type_traits>
 
@@ -23,15 +26,13 @@ namespace nvfp4 {
 namespace {
 
 constexpr int64_t kMaxH = 32768;   // 4 vectors of 8 values for each of 1024 threads
-constexpr int kWarpRowVecs = 128;  // rows of up to 128 vectors (1024 values) take a warp
-constexpr int kWarps = 8;          // warps of a CTA whose warps take a row each
+constexpr int kWarpRowVecs = 192;  // rows of up to 192 vectors (1536 values) take a warp
+constexpr int kWarps = 4;          // warps of a CTA whose warps take a row each
 
 enum { kPre = 0, kPreInt8 = 1, kPost = 2, kPostNext = 3, kQuant = 4 };
 
 struct NormParams {
-  const __nv_bfloat16 *x;         // [T, H]
   const __nv_bfloat16 *w;         // [H]
-  const __nv_bfloat16 *residual;  // [T, H]
   const __nv_bfloat16 *gate;      // null, or strides gt (0 or gh ? H : 1) and gh (0 or 1)
   const __nv_bfloat16 *w_next;    // [H]
   __nv_bfloat16 *out;             // [T, H]
@@ -43,13 +44,44 @@ struct NormParams {
   float eps, a;
 };
 
-__device__ __forceinline__ void unpack8(uint4 v, float (&f)[8]) {
-  f[0] = bf16_lo(v.x), f[1] = bf16_hi(v.x), f[2] = bf16_lo(v.y), f[3] = bf16_hi(v.y);
-  f[4] = bf16_lo(v.z), f[5] = bf16_hi(v.z), f[6] = bf16_lo(v.w), f[7] = bf16_hi(v.w);
+// Pairs of fp32 values: one instruction for both (fma, mul, add .f32x2), rounded as two.
+__device__ __forceinline__ uint64_t f2_bits(float2 a) {
+  return (uint64_t)__float_as_uint(a.x) | (uint64_t)__float_as_uint(a.y) << 32;
 }
-__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
-  return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                    pack_bf16x2(f[6], f[7]));
+__device__ __forceinline__ float2 f2_from(uint64_t v) {
+  return make_float2(__uint_as_float((uint32_t)v), __uint_as_float((uint32_t)(v >> 32)));
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(f2_bits(a)), "l"(f2_bits(b)), "l"(f2_bits(c)));
+  return f2_from(r);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(f2_bits(a)), "l"(f2_bits(b)));
+  return f2_from(r);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(f2_bits(a)), "l"(f2_bits(b)));
+  return f2_from(r);
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+// 8 bf16 values <-> 4 pairs of fp32
+__device__ __forceinline__ void unpack8(uint4 v, float2 (&f)[4]) {
+  f[0] = make_float2(bf16_lo(v.x), bf16_hi(v.x)), f[1] = make_float2(bf16_lo(v.y), bf16_hi(v.y));
+  f[2] = make_float2(bf16_lo(v.z), bf16_hi(v.z)), f[3] = make_float2(bf16_lo(v.w), bf16_hi(v.w));
+}
+__device__ __forceinline__ uint4 pack8(const float2 (&f)[4]) {
+  return make_uint4(pack_bf16x2(f[0].x, f[0].y), pack_bf16x2(f[1].x, f[1].y),
+                    pack_bf16x2(f[2].x, f[2].y), pack_bf16x2(f[3].x, f[3].y));
+}
+__device__ __forceinline__ uint4 ldg8(const __nv_bfloat16 *p, int c) {
+  return __ldg(reinterpret_cast<const uint4 *>(p) + c);
+}
+__device__ __forceinline__ void stg8(__nv_bfloat16 *p, int c, const float2 (&f)[4]) {
+  reinterpret_cast<uint4 *>(p)[c] = pack8(f);
 }
 
 struct Sum {
@@ -83,19 +115,51 @@ __device__ __forceinline__ void reduce_row(float (&v)[N], float *buf, int &turn)
   }
 }
 
-// Codes of 8 values: the integers nearest to 127 y / amax, ties to even.  For bf16 y both
-// 127 y and the distance of the quotient from a tie are exact to far below an fp32 ulp
-// (|p / q - (k + 1/2)| >= 1 / (2 q) for q < 2^8), so the fp32 quotient rounds as the real
-// one does.  `pre` is a power of two that keeps 127 y finite.
-__device__ __forceinline__ uint2 codes8(const float (&y)[8], float pre, float amax) {
+// Codes of 8 values: the integers nearest to 127 y / amax, ties to even, without a division
+// for each.  With inv = fl(127 / amax), v = fl(y inv) is off by at most 2^-23 relative.  A
+// quotient of 127 p / q with p, q < 2^8 (bf16 significands) and a power of two is either a tie
+// (k + 1/2, at most 9 bits) or at least 2^-16 relative away from one.  So v rounded to 18
+// significant bits (in its bit pattern) is the tie itself where there is one and stays on its
+// side otherwise, and rounding that to an integer rounds as the real quotient does.  Adding
+// 1.5 2^23 rounds to the integer, whose low byte is then the code.
+__device__ __forceinline__ uint32_t code_bits(float v) {
+  const uint32_t hi = (__float_as_uint(v) + 32u) & ~63u;
+  return __float_as_uint(__uint_as_float(hi) + 12582912.f);
+}
+__device__ __forceinline__ uint32_t low_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
+}
+__device__ __forceinline__ uint2 codes8(const float2 (&y)[4], float inv) {
   uint32_t q[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const float v = amax > 0.f ? __fdiv_rn(y[j] * pre * 127.f, amax) : 0.f;
-    q[j] = (uint32_t)(uint8_t)(int8_t)__float2int_rn(fminf(fmaxf(v, -127.f), 127.f));
+  for (int j = 0; j < 4; ++j) {
+    const float2 v = mul2(y[j], both(inv));
+    q[2 * j] = code_bits(v.x);
+    q[2 * j + 1] = code_bits(v.y);
   }
-  return make_uint2(q[0] | q[1] << 8 | q[2] << 16 | q[3] << 24,
-                    q[4] | q[5] << 8 | q[6] << 16 | q[7] << 24);
+  return make_uint2(low_bytes(q[0], q[1], q[2], q[3]), low_bytes(q[4], q[5], q[6], q[7]));
+}
+// Power of two that brings a row of this amax to where 127 / amax and its split neither
+// overflow nor underflow, and the scale of the row.
+__device__ __forceinline__ float code_range(float amax) {
+  return amax > 0x1p60f ? 0x1p-64f : amax < 0x1p-60f ? 0x1p+76f : 1.f;
+}
+__device__ __forceinline__ float code_inverse(float amax, float pre) {
+  return amax > 0.f ? __fdiv_rn(127.f, amax * pre) : 0.f;
+}
+__device__ __forceinline__ float code_scale(float amax) {
+  return amax > 0.f ? __fdiv_rn(amax, 127.f) : 1.f;
+}
+
+// CTAs that an SM holds: registers and shared memory are shared out for so
+// many.  Three against two or four: post_norm with next of 16384 x 6144, 140 us against 161
+// and 144; gradients of 4096 x 6144, 45 us against 52 (with a channel gate's column sums in
+// registers too, or four vectors a thread, two fit).
+constexpr int row_ctas(int maxt) { return maxt == 1024 ? 1 : maxt ? 3 : 6; }
+constexpr int grad_row_ctas(int maxt, int vpt, bool sum_g) {
+  if (maxt == 1024) return 1;
+  if (!maxt) return vpt <= 4 || !sum_g ? 4 : 3;
+  return vpt == 1 ? 4 : vpt == 4 || (vpt == 3 && sum_g) ? 2 : 3;
 }
 
 // MAXT: most threads of a CTA.  0 is a warp for each row, in CTAs of kWarps.
@@ -104,144 +168,211 @@ constexpr int max_threads() {
   return MAXT ? MAXT : kWarps * 32;
 }
 
-template <int VPT, int MAXT, int MODE>
-__global__ void __launch_bounds__(max_threads<MAXT>()) norm_kernel(NormParams p) {
-  constexpr bool WARP = MAXT == 0;
-  __shared__ float buf[2 * 32];
-  const int tpr = WARP ? 32 : blockDim.x;             // threads of a row
-  const int me = WARP ? (threadIdx.x & 31) : threadIdx.x;
-  const int nvec = p.H / 8;
-  const int64_t step = (int64_t)gridDim.x * (WARP ? blockDim.x / 32 : 1);
-  const float inv_h = 1.f / (float)p.H;
-  int turn = 0;
-  pdl_launch_dependents();
-  pdl_wait();
-  for (int64_t t = WARP ? (int64_t)blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5)
-                        : (int64_t)blockIdx.x;
-       t < p.T; t += step) {
-    uint4 xv[VPT], rv[VPT];
-    float ss[1] = {0.f};
+// ------------------------------------------------------------------ rows ahead
+constexpr int kMaxStages = 4;
+constexpr int kMaxArrays = 3;
+
+// The row arrays a kernel streams (bf16, H values a row).
+struct RowArrays {
+  const __nv_bfloat16 *p[kMaxArrays];
+  int n, stages;
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// Wait until at most `pending` of this thread's copy groups are in flight.
+__device__ __forceinline__ void cp_async_wait(int pending) {
+  if (pending >= 3) asm volatile("cp.async.wait_group 3;" ::: "memory");
+  else if (pending == 2) asm volatile("cp.async.wait_group 2;" ::: "memory");
+  else if (pending == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
+  else asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+
+// A thread's own slots: [stage][array][i] vectors, `pitch` bytes (16 a thread) apart.
+template <int VPT>
+struct RowFeed {
+  const RowArrays &a;
+  uint32_t base;
+  int me, tpr, nvec, pitch;
+  int64_t T, H;
+
+  __device__ __forceinline__ uint32_t slot(int stage, int arr, int i) const {
+    return base + (uint32_t)(((stage * a.n + arr) * VPT + i) * pitch);
+  }
+  __device__ __forceinline__ void fetch(int64_t t, int stage) const {
+    if (t < T) {
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int c = me + i * tpr;
-      xv[i] = rv[i] = make_uint4(0, 0, 0, 0);
-      if (c < nvec) {
-        xv[i] = ldg_stream(reinterpret_cast<const uint4 *>(p.x + t * p.H) + c);
-        if (MODE == kPost || MODE == kPostNext)
-          rv[i] = ldg_stream(reinterpret_cast<const uint4 *>(p.residual + t * p.H) + c);
-      }
-    }
-    if (MODE == kQuant) {
-      float am[1] = {0.f};
-#pragma unroll
-      for (int i = 0; i < VPT; ++i) {
-        float f[8];
-        unpack8(xv[i], f);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) am[0] = fmaxf(am[0], fabsf(f[j]));
-      }
-      reduce_row<WARP, Max>(am, buf, turn);
-      const float pre = am[0] > 1e30f ? 0x1p-64f : 1.f;
-#pragma unroll
-      for (int i = 0; i < VPT; ++i) {
-        const int c = me + i * tpr;
-        float f[8];
-        unpack8(xv[i], f);
-        if (c < nvec)
-          reinterpret_cast<uint2 *>(p.codes + t * p.H)[c] = codes8(f, pre, am[0] * pre);
-      }
-      if (me == 0) p.scales[t] = am[0] > 0.f ? __fdiv_rn(am[0], 127.f) : 1.f;
-      continue;
-    }
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      float f[8];
-      unpack8(xv[i], f);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) ss[0] = fmaf(f[j], f[j], ss[0]);
-    }
-    reduce_row<WARP, Sum>(ss, buf, turn);
-    const float r = rsqrtf(fmaf(ss[0], inv_h, p.eps));
-    if (MODE == kPre || MODE == kPreInt8) {
-      float am[1] = {0.f};
-      float y[VPT][8];
-#pragma unroll
-      for (int i = 0; i < VPT; ++i) {
-        const int c = me + i * tpr;
-        float w[8];
-        unpack8(xv[i], y[i]);
-        unpack8(c < nvec ? __ldg(reinterpret_cast<const uint4 *>(p.w) + c)
-                         : make_uint4(0, 0, 0, 0), w);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          y[i][j] = y[i][j] * r * w[j];
-          if (MODE == kPreInt8) am[0] = fmaxf(am[0], fabsf(y[i][j]));
-        }
-        if (MODE == kPre && c < nvec)
-          reinterpret_cast<uint4 *>(p.out + t * p.H)[c] = pack8(y[i]);
-      }
-      if (MODE == kPreInt8) {
-        reduce_row<WARP, Max>(am, buf, turn);
-        const float pre = am[0] > 1e30f ? 0x1p-64f : 1.f;
+      for (int k = 0; k < kMaxArrays; ++k)
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
           const int c = me + i * tpr;
-          if (c < nvec)
-            reinterpret_cast<uint2 *>(p.codes + t * p.H)[c] = codes8(y[i], pre, am[0] * pre);
+          if (k < a.n && c < nvec)
+            cp_async16(slot(stage, k, i), reinterpret_cast<const uint4 *>(a.p[k] + t * H) + c);
         }
-        if (me == 0) p.scales[t] = am[0] > 0.f ? __fdiv_rn(am[0], 127.f) : 1.f;
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+  __device__ __forceinline__ uint4 get(int stage, int arr, int i) const {
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (me + i * tpr < nvec)
+      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                   : "r"(slot(stage, arr, i))
+                   : "memory");
+    return v;
+  }
+};
+
+extern __shared__ __align__(16) unsigned char dyn_smem[];
+
+template <int VPT, int MAXT>
+__device__ __forceinline__ RowFeed<VPT> make_feed(const RowArrays &a, int64_t T, int64_t H) {
+  const int tpr = MAXT ? blockDim.x : 32;
+  return {a, (uint32_t)__cvta_generic_to_shared(dyn_smem) + threadIdx.x * 16,
+          (int)(MAXT ? threadIdx.x : threadIdx.x & 31), tpr, (int)(H / 8), (int)blockDim.x * 16,
+          T, H};
+}
+
+template <int VPT, int MAXT, int MODE>
+__global__ void __launch_bounds__(max_threads<MAXT>(), row_ctas(MAXT))
+    norm_kernel(const __grid_constant__ NormParams p, const __grid_constant__ RowArrays rows) {
+  constexpr bool WARP = MAXT == 0;
+  __shared__ float buf[2 * 32];
+  const RowFeed<VPT> feed = make_feed<VPT, MAXT>(rows, p.T, p.H);
+  const int me = feed.me, tpr = feed.tpr, nvec = feed.nvec;
+  const int64_t step = (int64_t)gridDim.x * (WARP ? kWarps : 1);
+  const int64_t t0 =
+      WARP ? (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5) : (int64_t)blockIdx.x;
+  const float inv_h = 1.f / (float)p.H;
+  int turn = 0, stage = 0;
+  pdl_launch_dependents();
+  pdl_wait();
+  for (int k = 0; k < rows.stages; ++k) feed.fetch(t0 + k * step, k);
+  for (int64_t t = t0; t < p.T; t += step) {
+    cp_async_wait(rows.stages - 1);
+    float r = 1.f;
+    if constexpr (MODE != kQuant) {
+      float2 sq = both(0.f);
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        float2 x[4];
+        unpack8(feed.get(stage, 0, i), x);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sq = fma2(x[j], x[j], sq);
       }
-    } else {
-      float o[VPT][8];
-      float s2[1] = {0.f};
-      const __nv_bfloat16 *grow = p.gate ? p.gate + t * p.gt : nullptr;
-      const float g1 = (grow && !p.gh) ? __bfloat162float(*grow) : 1.f;
+      float ss[1] = {sq.x + sq.y};
+      reduce_row<WARP, Sum>(ss, buf, turn);
+      r = rsqrtf(fmaf(ss[0], inv_h, p.eps));
+    }
+    if constexpr (MODE == kPre) {
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
         const int c = me + i * tpr;
-        const bool in = c < nvec;
-        float w[8], q[8], g[8];
-        unpack8(xv[i], o[i]);
-        unpack8(rv[i], q);
-        unpack8(in ? __ldg(reinterpret_cast<const uint4 *>(p.w) + c) : make_uint4(0, 0, 0, 0), w);
-        if (p.gh && in) {
-          unpack8(__ldg(reinterpret_cast<const uint4 *>(grow) + c), g);
+        if (c >= nvec) continue;
+        float2 y[4], w[4];
+        unpack8(feed.get(stage, 0, i), y);
+        unpack8(ldg8(p.w, c), w);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y[j] = mul2(mul2(y[j], both(r)), w[j]);
+        stg8(p.out + t * p.H, c, y);
+      }
+    } else if constexpr (MODE == kPreInt8 || MODE == kQuant) {
+      float am[1] = {0.f};
+      uint4 xv[MODE == kQuant ? VPT : 1];
+      float2 y[MODE == kPreInt8 ? VPT : 1][4];
+      if constexpr (MODE == kPreInt8) {
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+          const int c = me + i * tpr;
+          float2 w[4];
+          unpack8(feed.get(stage, 0, i), y[i]);
+          unpack8(c < nvec ? ldg8(p.w, c) : make_uint4(0, 0, 0, 0), w);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            y[i][j] = mul2(mul2(y[i][j], both(r)), w[j]);
+            am[0] = fmaxf(am[0], fmaxf(fabsf(y[i][j].x), fabsf(y[i][j].y)));
+          }
+        }
+      } else {   // the largest of two bf16 at a time, exact
+        __nv_bfloat162 m = __float2bfloat162_rn(0.f);
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+          xv[i] = feed.get(stage, 0, i);
+          const uint32_t u[4] = {xv[i].x, xv[i].y, xv[i].z, xv[i].w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            m = __hmax2(m, __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&u[j])));
+        }
+        am[0] = fmaxf(__low2float(m), __high2float(m));
+      }
+      reduce_row<WARP, Max>(am, buf, turn);
+      const float pre = code_range(am[0]), inv = code_inverse(am[0], pre);
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        const int c = me + i * tpr;
+        const int k = MODE == kPreInt8 ? i : 0;
+        if (MODE == kQuant) unpack8(xv[MODE == kQuant ? i : 0], y[k]);
+        if (pre != 1.f)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) y[k][j] = mul2(y[k][j], both(pre));
+        if (c < nvec) reinterpret_cast<uint2 *>(p.codes + t * p.H)[c] = codes8(y[k], inv);
+      }
+      if (me == 0) p.scales[t] = code_scale(am[0]);
+    } else {
+      float2 o[VPT][4];
+      float2 sq = both(0.f);
+      const float g1 = (p.gate && !p.gh) ? __bfloat162float(p.gate[t * p.gt]) : 1.f;
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        const int c = me + i * tpr;
+        if (c >= nvec) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) o[i][j] = both(0.f);
+          continue;
+        }
+        float2 w[4], q[4], g[4];
+        unpack8(feed.get(stage, 0, i), o[i]);
+        unpack8(feed.get(stage, 1, i), q);
+        unpack8(ldg8(p.w, c), w);
+        if (p.gh) {   // a gate for each value is a third row array
+          unpack8(p.gt ? feed.get(stage, 2, i) : ldg8(p.gate, c), g);
         } else {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) g[j] = g1;
+          for (int j = 0; j < 4; ++j) g[j] = both(g1);
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          o[i][j] = fmaf(g[j], o[i][j] * r * w[j], p.a * q[j]);
-          if (MODE == kPostNext) s2[0] = fmaf(in ? o[i][j] : 0.f, o[i][j], s2[0]);
+        for (int j = 0; j < 4; ++j) {
+          o[i][j] = fma2(g[j], mul2(mul2(o[i][j], both(r)), w[j]), mul2(both(p.a), q[j]));
+          if (MODE == kPostNext) sq = fma2(o[i][j], o[i][j], sq);
         }
-        if (in) reinterpret_cast<uint4 *>(p.out + t * p.H)[c] = pack8(o[i]);
+        stg8(p.out + t * p.H, c, o[i]);
       }
-      if (MODE == kPostNext) {
+      if constexpr (MODE == kPostNext) {
+        float s2[1] = {sq.x + sq.y};
         reduce_row<WARP, Sum>(s2, buf, turn);
         const float r2 = rsqrtf(fmaf(s2[0], inv_h, p.eps));
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
           const int c = me + i * tpr;
           if (c >= nvec) continue;
-          float w[8];
-          unpack8(__ldg(reinterpret_cast<const uint4 *>(p.w_next) + c), w);
+          float2 w[4];
+          unpack8(ldg8(p.w_next, c), w);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) w[j] *= o[i][j] * r2;
-          reinterpret_cast<uint4 *>(p.next + t * p.H)[c] = pack8(w);
+          for (int j = 0; j < 4; ++j) w[j] = mul2(w[j], mul2(o[i][j], both(r2)));
+          stg8(p.next + t * p.H, c, w);
         }
       }
     }
+    feed.fetch(t + rows.stages * step, stage);   // this thread has used its slots
+    stage = stage + 1 == rows.stages ? 0 : stage + 1;
   }
 }
 
 // ------------------------------------------------------------------ gradients
 struct NormGradParams {
-  const __nv_bfloat16 *d;      // [T, H]  gradient of the result
-  const __nv_bfloat16 *x;      // [T, H]
   const __nv_bfloat16 *w;      // [H]
   const __nv_bfloat16 *gate;   // as in NormParams
-  const __nv_bfloat16 *dskip;  // [T, H] added to dx, or null
   __nv_bfloat16 *dx;           // [T, H]
   __nv_bfloat16 *dres;         // [T, H] a * d, or null
   __nv_bfloat16 *dgate_el;     // [T, H] or [T, 1] gate gradient, or null
@@ -250,68 +381,66 @@ struct NormGradParams {
   int64_t T, gt;
   int H, gh;
   int sum_g;                   // 0: none, 1: [P, H] (gate [1, H]), 2: [P] (gate [1, 1])
+  int skip_at, gate_at;        // row array of dskip, of a gate for each value; 0: none
   float eps, a;
 };
 
-template <int VPT, int MAXT>
-__global__ void __launch_bounds__(max_threads<MAXT>()) norm_grad_kernel(NormGradParams p) {
+// Row arrays: x, the gradient of the result, then dskip and the gate where there are any.
+template <int VPT, int MAXT, bool SUMG>
+__global__ void __launch_bounds__(max_threads<MAXT>(), grad_row_ctas(MAXT, VPT, SUMG))
+    norm_grad_kernel(const __grid_constant__ NormGradParams p,
+                     const __grid_constant__ RowArrays rows) {
   constexpr bool WARP = MAXT == 0;
   __shared__ float buf[2 * 32 * 2];
-  extern __shared__ float acc_s[];   // WARP: [2][H] sums of the CTA's warps
-  const int tpr = WARP ? 32 : blockDim.x;
-  const int me = WARP ? (threadIdx.x & 31) : threadIdx.x;
-  const int nvec = p.H / 8;
-  const int64_t step = (int64_t)gridDim.x * (WARP ? blockDim.x / 32 : 1);
+  const RowFeed<VPT> feed = make_feed<VPT, MAXT>(rows, p.T, p.H);
+  const int me = feed.me, tpr = feed.tpr, nvec = feed.nvec;
+  const int64_t step = (int64_t)gridDim.x * (WARP ? kWarps : 1);
+  const int64_t t0 =
+      WARP ? (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5) : (int64_t)blockIdx.x;
   const float inv_h = 1.f / (float)p.H;
-  int turn = 0;
-  float aw[VPT][8], ag[VPT][8], a1 = 0.f;
+  int turn = 0, stage = 0;
+  float2 aw[VPT][4], ag[SUMG ? VPT : 1][4];
+  float a1 = 0.f;
 #pragma unroll
   for (int i = 0; i < VPT; ++i)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) aw[i][j] = ag[i][j] = 0.f;
+    for (int j = 0; j < 4; ++j) {
+      aw[i][j] = both(0.f);
+      if (SUMG) ag[i][j] = both(0.f);
+    }
   pdl_launch_dependents();
   pdl_wait();
-  for (int64_t t = WARP ? (int64_t)blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5)
-                        : (int64_t)blockIdx.x;
-       t < p.T; t += step) {
-    uint4 xv[VPT], dv[VPT];
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int c = me + i * tpr;
-      xv[i] = dv[i] = make_uint4(0, 0, 0, 0);
-      if (c < nvec) {
-        xv[i] = ldg_stream(reinterpret_cast<const uint4 *>(p.x + t * p.H) + c);
-        dv[i] = ldg_stream(reinterpret_cast<const uint4 *>(p.d + t * p.H) + c);
-      }
-    }
-    const __nv_bfloat16 *grow = p.gate ? p.gate + t * p.gt : nullptr;
-    const float g1 = (grow && !p.gh) ? __bfloat162float(*grow) : 1.f;
-    // s[0] = sum x^2, s[1] = sum d w x (times the gate where it has a value for each channel)
-    float s[2] = {0.f, 0.f};
+  for (int k = 0; k < rows.stages; ++k) feed.fetch(t0 + k * step, k);
+  for (int64_t t = t0; t < p.T; t += step) {
+    cp_async_wait(rows.stages - 1);
+    const float g1 = (p.gate && !p.gh) ? __bfloat162float(p.gate[t * p.gt]) : 1.f;
+    // sums of x^2, and of d w x (times the gate where it has a value for each channel)
+    float2 sx = both(0.f), sd = both(0.f);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int c = me + i * tpr;
       if (c >= nvec) continue;
-      float x[8], d[8], w[8];
-      unpack8(xv[i], x);
-      unpack8(dv[i], d);
-      unpack8(__ldg(reinterpret_cast<const uint4 *>(p.w) + c), w);
+      float2 x[4], d[4], w[4];
+      unpack8(feed.get(stage, 0, i), x);
+      unpack8(feed.get(stage, 1, i), d);
+      unpack8(ldg8(p.w, c), w);
       if (p.gh) {
-        float g[8];
-        unpack8(__ldg(reinterpret_cast<const uint4 *>(grow) + c), g);
+        float2 g[4];
+        unpack8(p.gate_at ? feed.get(stage, p.gate_at, i) : ldg8(p.gate, c), g);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) w[j] *= g[j];
+        for (int j = 0; j < 4; ++j) w[j] = mul2(w[j], g[j]);
       }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        s[0] = fmaf(x[j], x[j], s[0]);
-        s[1] = fmaf(d[j] * w[j], x[j], s[1]);
+      for (int j = 0; j < 4; ++j) {
+        sx = fma2(x[j], x[j], sx);
+        sd = fma2(mul2(d[j], w[j]), x[j], sd);
       }
     }
+    float s[2] = {sx.x + sx.y, sd.x + sd.y};
     reduce_row<WARP, Sum>(s, buf, turn);
     const float r = rsqrtf(fmaf(s[0], inv_h, p.eps));
     const float m = r * s[1] * inv_h * g1;   // mean(dn n)
-    if (grow && !p.gh) {
+    if (p.gate && !p.gh) {
       if (p.sum_g == 2)
         a1 += r * s[1];
       else if (me == 0 && p.dgate_el)
@@ -321,53 +450,59 @@ __global__ void __launch_bounds__(max_threads<MAXT>()) norm_grad_kernel(NormGrad
     for (int i = 0; i < VPT; ++i) {
       const int c = me + i * tpr;
       if (c >= nvec) continue;
-      float x[8], d[8], w[8], g[8], o[8], e[8];
-      unpack8(xv[i], x);
-      unpack8(dv[i], d);
-      unpack8(__ldg(reinterpret_cast<const uint4 *>(p.w) + c), w);
+      float2 x[4], d[4], w[4], g[4], o[4], e[4];
+      unpack8(feed.get(stage, 0, i), x);   // read again: registers hold the column sums
+      unpack8(feed.get(stage, 1, i), d);
+      unpack8(ldg8(p.w, c), w);
       if (p.gh) {
-        unpack8(__ldg(reinterpret_cast<const uint4 *>(grow) + c), g);
+        unpack8(p.gate_at ? feed.get(stage, p.gate_at, i) : ldg8(p.gate, c), g);
       } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) g[j] = g1;
+        for (int j = 0; j < 4; ++j) g[j] = both(g1);
       }
-      if (p.dskip) {
-        unpack8(ldg_stream(reinterpret_cast<const uint4 *>(p.dskip + t * p.H) + c), o);
+      if (p.skip_at) {
+        unpack8(feed.get(stage, p.skip_at, i), o);
       } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) o[j] = 0.f;
+        for (int j = 0; j < 4; ++j) o[j] = both(0.f);
       }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float n = x[j] * r;
-        e[j] = d[j] * w[j] * n;
-        aw[i][j] = fmaf(d[j] * g[j], n, aw[i][j]);
-        if (p.sum_g == 1) ag[i][j] += e[j];
-        o[j] += r * (d[j] * g[j] * w[j] - n * m);
+      for (int j = 0; j < 4; ++j) {
+        const float2 n = mul2(x[j], both(r)), dg = mul2(d[j], g[j]);
+        if (SUMG || p.dgate_el) e[j] = mul2(mul2(d[j], w[j]), n);
+        aw[i][j] = fma2(dg, n, aw[i][j]);
+        if (SUMG) ag[i][j] = add2(ag[i][j], e[j]);
+        o[j] = fma2(both(r), fma2(dg, w[j], mul2(n, both(-m))), o[j]);
       }
-      reinterpret_cast<uint4 *>(p.dx + t * p.H)[c] = pack8(o);
-      if (p.gh && p.dgate_el) reinterpret_cast<uint4 *>(p.dgate_el + t * p.H)[c] = pack8(e);
+      stg8(p.dx + t * p.H, c, o);
+      if (p.gh && p.dgate_el) stg8(p.dgate_el + t * p.H, c, e);
       if (p.dres) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) d[j] *= p.a;
-        reinterpret_cast<uint4 *>(p.dres + t * p.H)[c] = pack8(d);
+        for (int j = 0; j < 4; ++j) d[j] = mul2(d[j], both(p.a));
+        stg8(p.dres + t * p.H, c, d);
       }
     }
+    feed.fetch(t + rows.stages * step, stage);
+    stage = stage + 1 == rows.stages ? 0 : stage + 1;
   }
   // this CTA's sums, always in the same order
   if (WARP) {
+    float *acc_s = reinterpret_cast<float *>(dyn_smem);   // [2][H]; the slots are empty
     const int warp = threadIdx.x >> 5;
-    for (int w = 0; w < (int)(blockDim.x / 32); ++w) {
+    cp_async_wait(0);
+    __syncthreads();
+    for (int w = 0; w < kWarps; ++w) {
       if (warp == w) {
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
           const int c = me + i * 32;
           if (c >= nvec) continue;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            acc_s[c * 8 + j] = w ? acc_s[c * 8 + j] + aw[i][j] : aw[i][j];
-            if (p.sum_g == 1)
-              acc_s[p.H + c * 8 + j] = w ? acc_s[p.H + c * 8 + j] + ag[i][j] : ag[i][j];
+          for (int j = 0; j < 4; ++j) {
+            float2 *at = reinterpret_cast<float2 *>(acc_s + c * 8 + 2 * j);
+            *at = w ? add2(*at, aw[i][j]) : aw[i][j];
+            at = reinterpret_cast<float2 *>(acc_s + p.H + c * 8 + 2 * j);
+            if (SUMG) *at = w ? add2(*at, ag[i][j]) : ag[i][j];
           }
         }
         if (me == 0) buf[0] = w ? buf[0] + a1 : a1;
@@ -376,7 +511,7 @@ __global__ void __launch_bounds__(max_threads<MAXT>()) norm_grad_kernel(NormGrad
     }
     for (int c = threadIdx.x; c < p.H; c += blockDim.x) {
       p.part_w[(int64_t)blockIdx.x * p.H + c] = acc_s[c];
-      if (p.sum_g == 1) p.part_g[(int64_t)blockIdx.x * p.H + c] = acc_s[p.H + c];
+      if (SUMG) p.part_g[(int64_t)blockIdx.x * p.H + c] = acc_s[p.H + c];
     }
     if (p.sum_g == 2 && threadIdx.x == 0) p.part_g[blockIdx.x] = buf[0];
   } else {
@@ -385,44 +520,64 @@ __global__ void __launch_bounds__(max_threads<MAXT>()) norm_grad_kernel(NormGrad
       const int c = me + i * tpr;
       if (c >= nvec) continue;
       float4 *o = reinterpret_cast<float4 *>(p.part_w + (int64_t)blockIdx.x * p.H + c * 8);
-      o[0] = make_float4(aw[i][0], aw[i][1], aw[i][2], aw[i][3]);
-      o[1] = make_float4(aw[i][4], aw[i][5], aw[i][6], aw[i][7]);
-      if (p.sum_g == 1) {
+      o[0] = make_float4(aw[i][0].x, aw[i][0].y, aw[i][1].x, aw[i][1].y);
+      o[1] = make_float4(aw[i][2].x, aw[i][2].y, aw[i][3].x, aw[i][3].y);
+      if (SUMG) {
         o = reinterpret_cast<float4 *>(p.part_g + (int64_t)blockIdx.x * p.H + c * 8);
-        o[0] = make_float4(ag[i][0], ag[i][1], ag[i][2], ag[i][3]);
-        o[1] = make_float4(ag[i][4], ag[i][5], ag[i][6], ag[i][7]);
+        o[0] = make_float4(ag[i][0].x, ag[i][0].y, ag[i][1].x, ag[i][1].y);
+        o[1] = make_float4(ag[i][2].x, ag[i][2].y, ag[i][3].x, ag[i][3].y);
       }
     }
     if (p.sum_g == 2 && threadIdx.x == 0) p.part_g[blockIdx.x] = a1;
   }
 }
 
-// Column sums of the CTAs' partial sums: 32 columns by 8 slices of the P rows a CTA, the
-// slices added in order.  blockIdx.y 0: dweight, 1: the channel gate's gradient; the
-// gradient of a single gate is one more column sum, of [P, 1].
-__global__ void __launch_bounds__(256) norm_grad_sum_kernel(const float *part_w,
-                                                            const float *part_g, int P, int H,
-                                                            int gcols, __nv_bfloat16 *dw,
-                                                            __nv_bfloat16 *dg) {
-  __shared__ float s[8][32];
-  const int lane = threadIdx.x & 31, q = threadIdx.x >> 5;
+// Column sums of the CTAs' partial sums: 32 columns (16-byte loads of 4) by 128 slices of the
+// P rows a CTA, so that a thread's few loads are all in flight at once; the slices are added
+// in order.  blockIdx.y 0: dweight, 1: the channel gate's gradient, or in one CTA that of a
+// single gate (gcols 1): the sum of P values.
+__global__ void __launch_bounds__(1024) norm_grad_sum_kernel(const float *part_w,
+                                                             const float *part_g, int P, int H,
+                                                             int gcols, __nv_bfloat16 *dw,
+                                                             __nv_bfloat16 *dg) {
+  __shared__ float s[128][33];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const bool single = blockIdx.y && gcols == 1;
+  if (single && blockIdx.x) return;
   const float *part = blockIdx.y ? part_g : part_w;
-  __nv_bfloat16 *out = blockIdx.y ? dg : dw;
-  const int cols = blockIdx.y ? gcols : H;
-  const int c = blockIdx.x * 32 + lane;
   pdl_wait();
-  float v = 0.f;
-  if (c < cols) {
-#pragma unroll 4
-    for (int i = q; i < P; i += 8) v += part[(int64_t)i * cols + c];
-  }
-  s[q][lane] = v;
-  __syncthreads();
-  if (q == 0 && c < cols) {
+  if (single) {
+    float v = 0.f;
+    for (int i = threadIdx.x; i < P; i += 1024) v += part[i];
+    s[warp][lane] = v;
+    __syncthreads();
+    v = 0.f;
+    if (warp == 0)
+      for (int k = 0; k < 32; ++k) v += s[k][lane];
 #pragma unroll
-    for (int k = 1; k < 8; ++k) v += s[k][lane];
-    out[c] = __float2bfloat16_rn(v);
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    if (threadIdx.x == 0) dg[0] = __float2bfloat16_rn(v);
+    return;
   }
+  const int q = threadIdx.x >> 3, c = blockIdx.x * 32 + (threadIdx.x & 7) * 4;
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (c < H) {
+#pragma unroll 8
+    for (int i = q; i < P; i += 128) {
+      const float4 x = __ldg(reinterpret_cast<const float4 *>(part + (int64_t)i * H + c));
+      v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
+    }
+  }
+  float *at = &s[q][(threadIdx.x & 7) * 4];
+  at[0] = v.x, at[1] = v.y, at[2] = v.z, at[3] = v.w;
+  __syncthreads();
+  float t = s[lane][warp];   // warp w adds the 128 slices of column w
+#pragma unroll
+  for (int k = 1; k < 4; ++k) t += s[lane + 32 * k][warp];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
+  const int col = blockIdx.x * 32 + warp;
+  if (lane == 0 && col < H) (blockIdx.y ? dg : dw)[col] = __float2bfloat16_rn(t);
 }
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
@@ -451,42 +606,70 @@ int with_shape(const RowShape &rs, F f) {
       default: return f(std::integral_constant<int, 4>(), maxt);
     }
   };
-  if (rs.maxt == 0) return vpt(std::integral_constant<int, 0>());
+  if (rs.maxt == 0) {
+    const std::integral_constant<int, 0> warp;
+    if (rs.vpt == 5) return f(std::integral_constant<int, 5>(), warp);
+    if (rs.vpt == 6) return f(std::integral_constant<int, 6>(), warp);
+    return vpt(warp);
+  }
   if (rs.maxt == 256) return vpt(std::integral_constant<int, 256>());
   return vpt(std::integral_constant<int, 1024>());
 }
 
+// How many rows ahead a CTA fetches: what fits its share of an SM's shared memory when
+// `ctas` of them share it, at most kMaxStages.
+size_t plan_rows(RowArrays *rows, const RowShape &rs, int ctas) {
+  const size_t stage = (size_t)rows->n * rs.vpt * rs.threads * 16;
+  const size_t budget = 208 * 1024 / ctas;
+  rows->stages = (int)std::max<size_t>(1, std::min<size_t>(kMaxStages, budget / stage));
+  return stage * rows->stages;
+}
+
 template <int MODE>
-int launch_norm(const NormParams &p, cudaStream_t s) {
+int launch_norm(const NormParams &p, RowArrays rows, cudaStream_t s) {
   const RowShape rs = row_shape(p.H / 8, p.T < num_sms());
   const int64_t ctas = rs.maxt ? p.T : ceil_div(p.T, kWarps);
-  const dim3 grid((unsigned)std::min<int64_t>(ctas, (int64_t)1 << 30));
+  const size_t smem = plan_rows(&rows, rs, row_ctas(rs.maxt));
   return with_shape(rs, [&](auto vpt, auto maxt) {
-    return launch_pdl(norm_kernel<vpt(), maxt(), MODE>, grid, dim3(rs.threads), 0, s, p);
+    auto k = norm_kernel<vpt(), maxt(), MODE>;
+    const int nb = resident_blocks(k, rs.threads, smem);
+    if (nb <= 0) return (int)NVFP4_ECUDA;
+    const dim3 grid((unsigned)std::min<int64_t>(ctas, (int64_t)num_sms() * nb));
+    return launch_pdl(k, grid, dim3(rs.threads), smem, s, p, rows);
   });
 }
 
-constexpr int kGradCtasPerSm = 2;
+// Most CTAs of a gradient: their partial sums of H values stay within about 8 MB (three CTAs
+// an SM at least), so that writing and adding them is small beside the rows.
 int grad_ctas(int64_t T, int64_t H) {
   const int64_t per = H / 8 <= kWarpRowVecs ? kWarps : 1;
-  return (int)std::max<int64_t>(
-      1, std::min<int64_t>(ceil_div(T, per), (int64_t)num_sms() * kGradCtasPerSm));
+  const int64_t most = std::min<int64_t>(8, std::max<int64_t>(3, (2 << 20) / H / num_sms()));
+  return (int)std::max<int64_t>(1, std::min<int64_t>(ceil_div(T, per), num_sms() * most));
 }
 size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 
-int run_grad(NormGradParams &p, __nv_bfloat16 *dw, __nv_bfloat16 *dg_sum, void *ws,
-             cudaStream_t s) {
-  const int P = grad_ctas(p.T, p.H);
+int run_grad(NormGradParams &p, RowArrays rows, __nv_bfloat16 *dw, __nv_bfloat16 *dg_sum,
+             void *ws, cudaStream_t s) {
+  const int most = grad_ctas(p.T, p.H);
+  int P = most;
   p.part_w = static_cast<float *>(ws);
-  p.part_g = reinterpret_cast<float *>(static_cast<char *>(ws) + align256((size_t)P * p.H * 4));
+  p.part_g = reinterpret_cast<float *>(static_cast<char *>(ws) + align256((size_t)most * p.H * 4));
   const RowShape rs = row_shape(p.H / 8, p.T < num_sms());
-  const size_t smem = rs.maxt ? 0 : (size_t)p.H * 8;   // at most 8 KB
+  size_t smem = plan_rows(&rows, rs, grad_row_ctas(rs.maxt, rs.vpt, p.sum_g == 1));
+  if (!rs.maxt) smem = std::max(smem, (size_t)p.H * 8);   // the warps' sums of dweight and dgate
+  auto launch = [&](auto k) {
+    const int nb = resident_blocks(k, rs.threads, smem);
+    if (nb <= 0) return (int)NVFP4_ECUDA;
+    P = std::min(most, num_sms() * nb);
+    return launch_pdl(k, dim3(P), dim3(rs.threads), smem, s, p, rows);
+  };
   const int st = with_shape(rs, [&](auto vpt, auto maxt) {
-    return launch_pdl(norm_grad_kernel<vpt(), maxt()>, dim3(P), dim3(rs.threads), smem, s, p);
+    return p.sum_g == 1 ? launch(norm_grad_kernel<vpt(), maxt(), true>)
+                        : launch(norm_grad_kernel<vpt(), maxt(), false>);
   });
   if (st) return st;
   const dim3 grid((unsigned)ceil_div(p.H, 32), p.sum_g ? 2 : 1);
-  return launch_pdl(norm_grad_sum_kernel, grid, dim3(256), 0, s, (const float *)p.part_w,
+  return launch_pdl(norm_grad_sum_kernel, grid, dim3(1024), 0, s, (const float *)p.part_w,
                     (const float *)p.part_g, P, p.H, p.sum_g == 2 ? 1 : p.H, dw, dg_sum);
 }
 
@@ -532,8 +715,8 @@ extern "C" int moe_nvfp4_pre_norm(const __nv_bfloat16 *x, const __nv_bfloat16 *w
   if (T == 0) return NVFP4_OK;
   if (!x || !out || !aligned16(x) || !aligned16(out)) return NVFP4_EINVAL;
   NormParams p = {};
-  p.x = x, p.w = weight, p.out = out, p.T = T, p.H = (int)H, p.eps = eps;
-  return launch_norm<kPre>(p, stream);
+  p.w = weight, p.out = out, p.T = T, p.H = (int)H, p.eps = eps;
+  return launch_norm<kPre>(p, {{x}, 1}, stream);
 }
 
 extern "C" int moe_nvfp4_pre_norm_int8(const __nv_bfloat16 *x, const __nv_bfloat16 *weight,
@@ -547,8 +730,8 @@ extern "C" int moe_nvfp4_pre_norm_int8(const __nv_bfloat16 *x, const __nv_bfloat
       (reinterpret_cast<uintptr_t>(scales) & 3))
     return NVFP4_EINVAL;
   NormParams p = {};
-  p.x = x, p.w = weight, p.codes = codes, p.scales = scales, p.T = T, p.H = (int)H, p.eps = eps;
-  return launch_norm<kPreInt8>(p, stream);
+  p.w = weight, p.codes = codes, p.scales = scales, p.T = T, p.H = (int)H, p.eps = eps;
+  return launch_norm<kPreInt8>(p, {{x}, 1}, stream);
 }
 
 extern "C" int nvfp4_int8_quantize(const __nv_bfloat16 *x, int64_t rows, int64_t cols,
@@ -560,8 +743,8 @@ extern "C" int nvfp4_int8_quantize(const __nv_bfloat16 *x, int64_t rows, int64_t
       (reinterpret_cast<uintptr_t>(scales) & 3))
     return NVFP4_EINVAL;
   NormParams p = {};
-  p.x = x, p.codes = codes, p.scales = scales, p.T = rows, p.H = (int)cols;
-  return launch_norm<kQuant>(p, stream);
+  p.codes = codes, p.scales = scales, p.T = rows, p.H = (int)cols;
+  return launch_norm<kQuant>(p, {{x}, 1}, stream);
 }
 
 extern "C" int moe_nvfp4_post_norm(const __nv_bfloat16 *y, const __nv_bfloat16 *weight,
@@ -578,9 +761,10 @@ extern "C" int moe_nvfp4_post_norm(const __nv_bfloat16 *y, const __nv_bfloat16 *
   if (!y || !residual || !out || !aligned16(y) || !aligned16(residual) || !aligned16(out) ||
       (next_weight != nullptr) != (next != nullptr) || !aligned16(next))
     return NVFP4_EINVAL;
-  p.x = y, p.w = weight, p.residual = residual, p.w_next = next_weight, p.out = out;
+  p.w = weight, p.w_next = next_weight, p.out = out;
   p.next = next, p.T = T, p.H = (int)H, p.eps = eps, p.a = residual_scale;
-  return next ? launch_norm<kPostNext>(p, stream) : launch_norm<kPost>(p, stream);
+  const RowArrays rows = {{y, residual, gate}, p.gh && p.gt ? 3 : 2};
+  return next ? launch_norm<kPostNext>(p, rows, stream) : launch_norm<kPost>(p, rows, stream);
 }
 
 extern "C" size_t moe_nvfp4_norm_backward_workspace_size(int64_t T, int64_t H) {
@@ -603,9 +787,8 @@ extern "C" int moe_nvfp4_pre_norm_backward(const __nv_bfloat16 *dy, const __nv_b
       ws_bytes < moe_nvfp4_norm_backward_workspace_size(T, H))
     return NVFP4_EWORKSPACE;
   NormGradParams p = {};
-  p.d = dy, p.x = x, p.w = weight, p.dskip = dskip, p.dx = dx, p.T = T, p.H = (int)H;
-  p.eps = eps;
-  return run_grad(p, dweight, nullptr, workspace, stream);
+  p.w = weight, p.dx = dx, p.T = T, p.H = (int)H, p.eps = eps, p.skip_at = dskip ? 2 : 0;
+  return run_grad(p, {{x, dy, dskip}, dskip ? 3 : 2}, dweight, nullptr, workspace, stream);
 }
 
 extern "C" int moe_nvfp4_post_norm_backward(
@@ -632,9 +815,11 @@ extern "C" int moe_nvfp4_post_norm_backward(
       ws_bytes < moe_nvfp4_norm_backward_workspace_size(T, H))
     return NVFP4_EWORKSPACE;
   NormGradParams p = {};
-  p.d = dout, p.x = y, p.w = weight, p.gate = g.gate, p.dx = dy, p.dres = dresidual;
+  p.w = weight, p.gate = g.gate, p.dx = dy, p.dres = dresidual;
   p.T = T, p.gt = g.gt, p.gh = g.gh, p.H = (int)H, p.eps = eps, p.a = residual_scale;
   p.sum_g = gate && gate_rows == 1 ? (gate_cols == H ? 1 : 2) : 0;
   p.dgate_el = gate && gate_rows != 1 ? dgate : nullptr;
-  return run_grad(p, dweight, p.sum_g ? dgate : nullptr, workspace, stream);
+  p.gate_at = p.gh && p.gt ? 2 : 0;
+  return run_grad(p, {{y, dout, gate}, p.gate_at ? 3 : 2}, dweight, p.sum_g ? dgate : nullptr,
+                  workspace, stream);
 }
