@@ -92,7 +92,8 @@ struct Max {
 };
 
 // Reduce N values over the threads that share a row: a warp, or the CTA through `buf`
-// ([2][32][N]; the half alternates with `turn`, so one barrier a reduction is enough).
+// ([2][N][32]; the half alternates with `turn`, so one barrier a reduction is enough).  Both
+// operations have 0 for the warps that a CTA lacks (a maximum is one of magnitudes).
 template <bool WARP, typename Op, int N>
 __device__ __forceinline__ void reduce_row(float (&v)[N], float *buf, int &turn) {
 #pragma unroll
@@ -100,18 +101,29 @@ __device__ __forceinline__ void reduce_row(float (&v)[N], float *buf, int &turn)
 #pragma unroll
     for (int k = 0; k < N; ++k) v[k] = Op::op(v[k], __shfl_xor_sync(0xFFFFFFFFu, v[k], o));
   if (WARP) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = (int)(blockDim.x + 127) >> 7;
   float *b = buf + turn * 32 * N;
   turn ^= 1;
   if (lane == 0)
 #pragma unroll
-    for (int k = 0; k < N; ++k) b[warp * N + k] = v[k];
+    for (int k = 0; k < N; ++k) b[k * 32 + warp] = v[k];
   __syncthreads();
 #pragma unroll
   for (int k = 0; k < N; ++k) {
-    float s = b[k];
-    for (int w = 1; w < nw; ++w) s = Op::op(s, b[w * N + k]);
+    float s = 0.f;
+    for (int w = 0; w < nw; ++w) {
+      const float4 q = reinterpret_cast<const float4 *>(b + k * 32)[w];
+      s = Op::op(s, Op::op(Op::op(q.x, q.y), Op::op(q.z, q.w)));
+    }
     v[k] = s;
+  }
+}
+// Before the first reduction of a CTA: the places of warps that it lacks.
+template <bool WARP, int N>
+__device__ __forceinline__ void clear_reduce(float (&buf)[N]) {
+  if constexpr (!WARP) {
+    for (int k = threadIdx.x; k < N; k += blockDim.x) buf[k] = 0.f;
+    __syncthreads();
   }
 }
 
@@ -195,31 +207,33 @@ struct RowFeed {
   const RowArrays &a;
   uint32_t base;
   int me, tpr, nvec, pitch;
-  int64_t T, H;
+  int64_t T, row_bytes;
 
-  __device__ __forceinline__ uint32_t slot(int stage, int arr, int i) const {
-    return base + (uint32_t)(((stage * a.n + arr) * VPT + i) * pitch);
+  __device__ __forceinline__ uint32_t stage_at(int stage) const {
+    return base + (uint32_t)(stage * a.n * VPT * pitch);
   }
-  __device__ __forceinline__ void fetch(int64_t t, int stage) const {
+  __device__ __forceinline__ bool in(int i) const { return me + i * tpr < nvec; }
+  __device__ __forceinline__ void fetch(int64_t t, uint32_t at) const {
     if (t < T) {
+      const int64_t off = t * row_bytes + me * 16;
 #pragma unroll
-      for (int k = 0; k < kMaxArrays; ++k)
+      for (int k = 0; k < kMaxArrays; ++k) {
+        if (k >= a.n) break;
+        const char *src = reinterpret_cast<const char *>(a.p[k]) + off;
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-          const int c = me + i * tpr;
-          if (k < a.n && c < nvec)
-            cp_async16(slot(stage, k, i), reinterpret_cast<const uint4 *>(a.p[k] + t * H) + c);
-        }
+        for (int i = 0; i < VPT; ++i)
+          if (in(i)) cp_async16(at + (k * VPT + i) * pitch, src + i * tpr * 16);
+      }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   }
-  __device__ __forceinline__ uint4 get(int stage, int arr, int i) const {
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (me + i * tpr < nvec)
-      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                   : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                   : "r"(slot(stage, arr, i))
-                   : "memory");
+  // Vector i of array `arr` (only where in(i)).
+  __device__ __forceinline__ uint4 get(uint32_t at, int arr, int i) const {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(at + (arr * VPT + i) * pitch)
+                 : "memory");
     return v;
   }
 };
@@ -231,33 +245,36 @@ __device__ __forceinline__ RowFeed<VPT> make_feed(const RowArrays &a, int64_t T,
   const int tpr = MAXT ? blockDim.x : 32;
   return {a, (uint32_t)__cvta_generic_to_shared(dyn_smem) + threadIdx.x * 16,
           (int)(MAXT ? threadIdx.x : threadIdx.x & 31), tpr, (int)(H / 8), (int)blockDim.x * 16,
-          T, H};
+          T, H * 2};
 }
 
 template <int VPT, int MAXT, int MODE>
 __global__ void __launch_bounds__(max_threads<MAXT>(), row_ctas(MAXT))
     norm_kernel(const __grid_constant__ NormParams p, const __grid_constant__ RowArrays rows) {
   constexpr bool WARP = MAXT == 0;
-  __shared__ float buf[2 * 32];
+  __shared__ __align__(16) float buf[2 * 32];
   const RowFeed<VPT> feed = make_feed<VPT, MAXT>(rows, p.T, p.H);
-  const int me = feed.me, tpr = feed.tpr, nvec = feed.nvec;
+  const int me = feed.me, tpr = feed.tpr;
   const int64_t step = (int64_t)gridDim.x * (WARP ? kWarps : 1);
   const int64_t t0 =
       WARP ? (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5) : (int64_t)blockIdx.x;
   const float inv_h = 1.f / (float)p.H;
   int turn = 0, stage = 0;
+  clear_reduce<WARP>(buf);
   pdl_launch_dependents();
   pdl_wait();
-  for (int k = 0; k < rows.stages; ++k) feed.fetch(t0 + k * step, k);
+  for (int k = 0; k < rows.stages; ++k) feed.fetch(t0 + k * step, feed.stage_at(k));
   for (int64_t t = t0; t < p.T; t += step) {
     cp_async_wait(rows.stages - 1);
+    const uint32_t at = feed.stage_at(stage);
     float r = 1.f;
     if constexpr (MODE != kQuant) {
       float2 sq = both(0.f);
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
+        if (!feed.in(i)) continue;
         float2 x[4];
-        unpack8(feed.get(stage, 0, i), x);
+        unpack8(feed.get(at, 0, i), x);
 #pragma unroll
         for (int j = 0; j < 4; ++j) sq = fma2(x[j], x[j], sq);
       }
@@ -266,16 +283,17 @@ __global__ void __launch_bounds__(max_threads<MAXT>(), row_ctas(MAXT))
       r = rsqrtf(fmaf(ss[0], inv_h, p.eps));
     }
     if constexpr (MODE == kPre) {
+      __nv_bfloat16 *out = p.out + t * p.H;
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
+        if (!feed.in(i)) continue;
         const int c = me + i * tpr;
-        if (c >= nvec) continue;
         float2 y[4], w[4];
-        unpack8(feed.get(stage, 0, i), y);
+        unpack8(feed.get(at, 0, i), y);
         unpack8(ldg8(p.w, c), w);
 #pragma unroll
         for (int j = 0; j < 4; ++j) y[j] = mul2(mul2(y[j], both(r)), w[j]);
-        stg8(p.out + t * p.H, c, y);
+        stg8(out, c, y);
       }
     } else if constexpr (MODE == kPreInt8 || MODE == kQuant) {
       float am[1] = {0.f};
@@ -284,10 +302,10 @@ __global__ void __launch_bounds__(max_threads<MAXT>(), row_ctas(MAXT))
       if constexpr (MODE == kPreInt8) {
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-          const int c = me + i * tpr;
+          if (!feed.in(i)) continue;
           float2 w[4];
-          unpack8(feed.get(stage, 0, i), y[i]);
-          unpack8(c < nvec ? ldg8(p.w, c) : make_uint4(0, 0, 0, 0), w);
+          unpack8(feed.get(at, 0, i), y[i]);
+          unpack8(ldg8(p.w, me + i * tpr), w);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             y[i][j] = mul2(mul2(y[i][j], both(r)), w[j]);
@@ -298,7 +316,8 @@ __global__ void __launch_bounds__(max_threads<MAXT>(), row_ctas(MAXT))
         __nv_bfloat162 m = __float2bfloat162_rn(0.f);
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-          xv[i] = feed.get(stage, 0, i);
+          if (!feed.in(i)) continue;
+          xv[i] = feed.get(at, 0, i);
           const uint32_t u[4] = {xv[i].x, xv[i].y, xv[i].z, xv[i].w};
 #pragma unroll
           for (int j = 0; j < 4; ++j)
@@ -308,63 +327,63 @@ __global__ void __launch_bounds__(max_threads<MAXT>(), row_ctas(MAXT))
       }
       reduce_row<WARP, Max>(am, buf, turn);
       const float pre = code_range(am[0]), inv = code_inverse(am[0], pre);
+      uint2 *out = reinterpret_cast<uint2 *>(p.codes + t * p.H);
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
-        const int c = me + i * tpr;
+        if (!feed.in(i)) continue;
         const int k = MODE == kPreInt8 ? i : 0;
         if (MODE == kQuant) unpack8(xv[MODE == kQuant ? i : 0], y[k]);
         if (pre != 1.f)
 #pragma unroll
           for (int j = 0; j < 4; ++j) y[k][j] = mul2(y[k][j], both(pre));
-        if (c < nvec) reinterpret_cast<uint2 *>(p.codes + t * p.H)[c] = codes8(y[k], inv);
+        out[me + i * tpr] = codes8(y[k], inv);
       }
       if (me == 0) p.scales[t] = code_scale(am[0]);
     } else {
       float2 o[VPT][4];
       float2 sq = both(0.f);
       const float g1 = (p.gate && !p.gh) ? __bfloat162float(p.gate[t * p.gt]) : 1.f;
+      const float rg = p.gh ? r : r * g1;   // a row's single gate goes with its norm
+      __nv_bfloat16 *out = p.out + t * p.H;
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
+        if (!feed.in(i)) continue;
         const int c = me + i * tpr;
-        if (c >= nvec) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) o[i][j] = both(0.f);
-          continue;
-        }
-        float2 w[4], q[4], g[4];
-        unpack8(feed.get(stage, 0, i), o[i]);
-        unpack8(feed.get(stage, 1, i), q);
+        float2 w[4], q[4];
+        unpack8(feed.get(at, 0, i), o[i]);
+        unpack8(feed.get(at, 1, i), q);
         unpack8(ldg8(p.w, c), w);
         if (p.gh) {   // a gate for each value is a third row array
-          unpack8(p.gt ? feed.get(stage, 2, i) : ldg8(p.gate, c), g);
-        } else {
+          float2 g[4];
+          unpack8(p.gt ? feed.get(at, 2, i) : ldg8(p.gate, c), g);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) g[j] = both(g1);
+          for (int j = 0; j < 4; ++j) w[j] = mul2(w[j], g[j]);
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          o[i][j] = fma2(g[j], mul2(mul2(o[i][j], both(r)), w[j]), mul2(both(p.a), q[j]));
+          o[i][j] = fma2(mul2(o[i][j], both(rg)), w[j], mul2(both(p.a), q[j]));
           if (MODE == kPostNext) sq = fma2(o[i][j], o[i][j], sq);
         }
-        stg8(p.out + t * p.H, c, o[i]);
+        stg8(out, c, o[i]);
       }
       if constexpr (MODE == kPostNext) {
         float s2[1] = {sq.x + sq.y};
         reduce_row<WARP, Sum>(s2, buf, turn);
         const float r2 = rsqrtf(fmaf(s2[0], inv_h, p.eps));
+        out = p.next + t * p.H;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
+          if (!feed.in(i)) continue;
           const int c = me + i * tpr;
-          if (c >= nvec) continue;
           float2 w[4];
           unpack8(ldg8(p.w_next, c), w);
 #pragma unroll
           for (int j = 0; j < 4; ++j) w[j] = mul2(w[j], mul2(o[i][j], both(r2)));
-          stg8(p.next + t * p.H, c, w);
+          stg8(out, c, w);
         }
       }
     }
-    feed.fetch(t + rows.stages * step, stage);   // this thread has used its slots
+    feed.fetch(t + rows.stages * step, at);   // this thread has used its slots
     stage = stage + 1 == rows.stages ? 0 : stage + 1;
   }
 }
@@ -378,20 +397,24 @@ struct NormGradParams {
   __nv_bfloat16 *dgate_el;     // [T, H] or [T, 1] gate gradient, or null
   float *part_w;               // [P, H] sums over a CTA's rows
   float *part_g;               // [P, H] of the channel gate's gradient, or [P] of a single one's
-  int64_t T, gt;
+  int64_t T, gt;               // gt, gh: as in NormParams
   int H, gh;
   int sum_g;                   // 0: none, 1: [P, H] (gate [1, H]), 2: [P] (gate [1, 1])
-  int skip_at, gate_at;        // row array of dskip, of a gate for each value; 0: none
+  int skip;                    // the third row array is dskip
   float eps, a;
 };
 
+// What the gate is: none, one for a row ([T, 1], [1, 1]), one for a channel ([1, H]: its
+// gradient is a column sum), one for each value.
+enum { kNoGate = 0, kRowGate = 1, kChannelGate = 2, kFullGate = 3 };
+
 // Row arrays: x, the gradient of the result, then dskip and the gate where there are any.
-template <int VPT, int MAXT, bool SUMG>
-__global__ void __launch_bounds__(max_threads<MAXT>(), grad_row_ctas(MAXT, VPT, SUMG))
+template <int VPT, int MAXT, int GATE>
+__global__ void __launch_bounds__(max_threads<MAXT>(), grad_row_ctas(MAXT, VPT, GATE == kChannelGate))
     norm_grad_kernel(const __grid_constant__ NormGradParams p,
                      const __grid_constant__ RowArrays rows) {
-  constexpr bool WARP = MAXT == 0;
-  __shared__ float buf[2 * 32 * 2];
+  constexpr bool WARP = MAXT == 0, SUMG = GATE == kChannelGate;
+  __shared__ __align__(16) float buf[2 * 32 * 2];
   const RowFeed<VPT> feed = make_feed<VPT, MAXT>(rows, p.T, p.H);
   const int me = feed.me, tpr = feed.tpr, nvec = feed.nvec;
   const int64_t step = (int64_t)gridDim.x * (WARP ? kWarps : 1);
@@ -399,6 +422,7 @@ __global__ void __launch_bounds__(max_threads<MAXT>(), grad_row_ctas(MAXT, VPT, 
       WARP ? (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5) : (int64_t)blockIdx.x;
   const float inv_h = 1.f / (float)p.H;
   int turn = 0, stage = 0;
+  clear_reduce<WARP>(buf);
   float2 aw[VPT][4], ag[SUMG ? VPT : 1][4];
   float a1 = 0.f;
 #pragma unroll
@@ -410,23 +434,23 @@ __global__ void __launch_bounds__(max_threads<MAXT>(), grad_row_ctas(MAXT, VPT, 
     }
   pdl_launch_dependents();
   pdl_wait();
-  for (int k = 0; k < rows.stages; ++k) feed.fetch(t0 + k * step, k);
+  for (int k = 0; k < rows.stages; ++k) feed.fetch(t0 + k * step, feed.stage_at(k));
   for (int64_t t = t0; t < p.T; t += step) {
     cp_async_wait(rows.stages - 1);
-    const float g1 = (p.gate && !p.gh) ? __bfloat162float(p.gate[t * p.gt]) : 1.f;
+    const uint32_t at = feed.stage_at(stage);
     // sums of x^2, and of d w x (times the gate where it has a value for each channel)
     float2 sx = both(0.f), sd = both(0.f);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
+      if (!feed.in(i)) continue;
       const int c = me + i * tpr;
-      if (c >= nvec) continue;
       float2 x[4], d[4], w[4];
-      unpack8(feed.get(stage, 0, i), x);
-      unpack8(feed.get(stage, 1, i), d);
+      unpack8(feed.get(at, 0, i), x);
+      unpack8(feed.get(at, 1, i), d);
       unpack8(ldg8(p.w, c), w);
-      if (p.gh) {
+      if (GATE >= kChannelGate) {
         float2 g[4];
-        unpack8(p.gate_at ? feed.get(stage, p.gate_at, i) : ldg8(p.gate, c), g);
+        unpack8(GATE == kFullGate ? feed.get(at, 2, i) : ldg8(p.gate, c), g);
 #pragma unroll
         for (int j = 0; j < 4; ++j) w[j] = mul2(w[j], g[j]);
       }
@@ -439,50 +463,59 @@ __global__ void __launch_bounds__(max_threads<MAXT>(), grad_row_ctas(MAXT, VPT, 
     float s[2] = {sx.x + sx.y, sd.x + sd.y};
     reduce_row<WARP, Sum>(s, buf, turn);
     const float r = rsqrtf(fmaf(s[0], inv_h, p.eps));
-    const float m = r * s[1] * inv_h * g1;   // mean(dn n)
-    if (p.gate && !p.gh) {
+    const float g1 = GATE == kRowGate ? __bfloat162float(p.gate[t * p.gt]) : 1.f;
+    const float rg = r * g1;
+    const float k = rg * r * (r * s[1] * inv_h);   // r mean(dn n) r: dx = r dn - k x
+    if (GATE == kRowGate) {
       if (p.sum_g == 2)
         a1 += r * s[1];
-      else if (me == 0 && p.dgate_el)
+      else if (me == 0)
         p.dgate_el[t] = __float2bfloat16_rn(r * s[1]);
     }
+    const int64_t row = t * p.H;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
+      if (!feed.in(i)) continue;
       const int c = me + i * tpr;
-      if (c >= nvec) continue;
-      float2 x[4], d[4], w[4], g[4], o[4], e[4];
-      unpack8(feed.get(stage, 0, i), x);   // read again: registers hold the column sums
-      unpack8(feed.get(stage, 1, i), d);
+      float2 x[4], d[4], w[4], o[4];
+      unpack8(feed.get(at, 0, i), x);   // read again: registers hold the column sums
+      unpack8(feed.get(at, 1, i), d);
       unpack8(ldg8(p.w, c), w);
-      if (p.gh) {
-        unpack8(p.gate_at ? feed.get(stage, p.gate_at, i) : ldg8(p.gate, c), g);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) g[j] = both(g1);
-      }
-      if (p.skip_at) {
-        unpack8(feed.get(stage, p.skip_at, i), o);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) o[j] = both(0.f);
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 n = mul2(x[j], both(r)), dg = mul2(d[j], g[j]);
-        if (SUMG || p.dgate_el) e[j] = mul2(mul2(d[j], w[j]), n);
-        aw[i][j] = fma2(dg, n, aw[i][j]);
-        if (SUMG) ag[i][j] = add2(ag[i][j], e[j]);
-        o[j] = fma2(both(r), fma2(dg, w[j], mul2(n, both(-m))), o[j]);
-      }
-      stg8(p.dx + t * p.H, c, o);
-      if (p.gh && p.dgate_el) stg8(p.dgate_el + t * p.H, c, e);
       if (p.dres) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) d[j] = mul2(d[j], both(p.a));
-        stg8(p.dres + t * p.H, c, d);
+        for (int j = 0; j < 4; ++j) o[j] = mul2(d[j], both(p.a));
+        stg8(p.dres + row, c, o);
       }
+      float2 n[4];   // x r, and the row's single gate (dweight = sum d g n)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) n[j] = mul2(x[j], both(rg));
+      if (GATE >= kChannelGate) {
+        float2 g[4];
+        unpack8(GATE == kFullGate ? feed.get(at, 2, i) : ldg8(p.gate, c), g);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 dw = mul2(d[j], w[j]);
+          d[j] = mul2(d[j], g[j]);
+          if (SUMG) ag[i][j] = fma2(dw, n[j], ag[i][j]);
+          if (GATE == kFullGate) o[j] = mul2(dw, n[j]);
+        }
+        if (GATE == kFullGate) stg8(p.dgate_el + row, c, o);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) aw[i][j] = fma2(d[j], n[j], aw[i][j]);
+      if (p.skip) {
+        unpack8(feed.get(at, 2, i), o);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[j] = fma2(mul2(d[j], w[j]), both(rg), o[j]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[j] = mul2(mul2(d[j], w[j]), both(rg));
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[j] = fma2(x[j], both(-k), o[j]);
+      stg8(p.dx + row, c, o);
     }
-    feed.fetch(t + rows.stages * step, stage);
+    feed.fetch(t + rows.stages * step, at);
     stage = stage + 1 == rows.stages ? 0 : stage + 1;
   }
   // this CTA's sums, always in the same order
@@ -664,8 +697,10 @@ int run_grad(NormGradParams &p, RowArrays rows, __nv_bfloat16 *dw, __nv_bfloat16
     return launch_pdl(k, dim3(P), dim3(rs.threads), smem, s, p, rows);
   };
   const int st = with_shape(rs, [&](auto vpt, auto maxt) {
-    return p.sum_g == 1 ? launch(norm_grad_kernel<vpt(), maxt(), true>)
-                        : launch(norm_grad_kernel<vpt(), maxt(), false>);
+    if (!p.gate) return launch(norm_grad_kernel<vpt(), maxt(), kNoGate>);
+    if (!p.gh) return launch(norm_grad_kernel<vpt(), maxt(), kRowGate>);
+    if (!p.gt) return launch(norm_grad_kernel<vpt(), maxt(), kChannelGate>);
+    return launch(norm_grad_kernel<vpt(), maxt(), kFullGate>);
   });
   if (st) return st;
   const dim3 grid((unsigned)ceil_div(p.H, 32), p.sum_g ? 2 : 1);
@@ -787,7 +822,7 @@ extern "C" int moe_nvfp4_pre_norm_backward(const __nv_bfloat16 *dy, const __nv_b
       ws_bytes < moe_nvfp4_norm_backward_workspace_size(T, H))
     return NVFP4_EWORKSPACE;
   NormGradParams p = {};
-  p.w = weight, p.dx = dx, p.T = T, p.H = (int)H, p.eps = eps, p.skip_at = dskip ? 2 : 0;
+  p.w = weight, p.dx = dx, p.T = T, p.H = (int)H, p.eps = eps, p.skip = dskip != nullptr;
   return run_grad(p, {{x, dy, dskip}, dskip ? 3 : 2}, dweight, nullptr, workspace, stream);
 }
 
@@ -819,7 +854,6 @@ extern "C" int moe_nvfp4_post_norm_backward(
   p.T = T, p.gt = g.gt, p.gh = g.gh, p.H = (int)H, p.eps = eps, p.a = residual_scale;
   p.sum_g = gate && gate_rows == 1 ? (gate_cols == H ? 1 : 2) : 0;
   p.dgate_el = gate && gate_rows != 1 ? dgate : nullptr;
-  p.gate_at = p.gh && p.gt ? 2 : 0;
-  return run_grad(p, {{y, dout, gate}, p.gate_at ? 3 : 2}, dweight, p.sum_g ? dgate : nullptr,
+  return run_grad(p, {{y, dout, gate}, p.gh && p.gt ? 3 : 2}, dweight, p.sum_g ? dgate : nullptr,
                   workspace, stream);
 }
