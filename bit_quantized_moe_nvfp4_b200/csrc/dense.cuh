@@ -53,6 +53,7 @@ struct DenseArgs {
   int save_gu;                 // pair kernel, kEpiGate: tensor maps g / u are set
   int32_t *flag;               // error bits, or null
   int m_tiles, n_tiles;
+  int whole, cut, items;       // pair kernel: see item_at
 };
 
 // Bounded wait of one CTA; after any of its waits has given up, later ones return at once.
@@ -67,7 +68,22 @@ struct CtaWait {
     report_timeout(flag);
     return false;
   }
+  // The same for a converged warp: one answer for all lanes.
+  __device__ __forceinline__ bool warp(uint64_t *bar, uint32_t parity) const {
+    return __all_sync(0xFFFFFFFFu, (*this)(bar, parity));
+  }
 };
+
+// One lane of a converged warp, always the same one.  The issuing warps run their loops with
+// all lanes and elect one around each group of tensor or copy instructions: those take their
+// operands from the warp's uniform registers, and from inside a divergent branch each of them
+// needs its operands moved there one at a time (the 256 x 256 tiles ran 12% slower so).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+               : "=r"(p));
+  return p != 0;
+}
 
 // ------------------------------------------------------------------ pairs of CTAs
 constexpr int kPS = 6;                              // stages
@@ -79,6 +95,25 @@ constexpr uint32_t kPMisc = kPBars + 8 * (2 * kPS + 4);
 constexpr uint32_t kPSmem = kPMisc + 16 + 1024;
 constexpr int kPThreads = 192;                      // producer, MMA, 4 epilogue warps
 static_assert(kPSmem <= 227 * 1024, "shared memory budget");
+
+// What work item `i` is.  The first p.whole items are whole tiles, one after another to each
+// pair; the tiles that are left, too few to keep all pairs busy, are cut into `cut` items of
+// 256 / cut columns each (launch_pair), so the last round is that much shorter.
+struct PairItem {
+  int mt, nt, part, width;   // tile, part of it, columns of the part
+};
+__device__ __forceinline__ void tile_at(int i, int m_tiles, int n_tiles, int &mt, int &nt);
+__device__ __forceinline__ PairItem item_at(int i, const DenseArgs &p) {
+  PairItem t = {0, 0, 0, 256};
+  int tile = i;
+  if (i >= p.whole) {
+    t.part = (i - p.whole) % p.cut;
+    t.width = 256 / p.cut;
+    tile = p.whole + (i - p.whole) / p.cut;
+  }
+  tile_at(tile, p.m_tiles, p.n_tiles, t.mt, t.nt);
+  return t;
+}
 
 // Tile `i` of m_tiles x n_tiles, in groups of 8 rows of tiles, so that the tiles in flight at
 // one time share A and B tiles in L2.
@@ -150,25 +185,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
   pdl_wait();
 
   const CtaWait wait{abort, p.flag};
-  const int total = p.m_tiles * p.n_tiles, pairs = (int)gridDim.x / 2;
+  const int total = p.items, pairs = (int)gridDim.x / 2;
   const int first = (int)blockIdx.x / 2;
   constexpr int kElems = KIND == kS8 ? 128 : 64;   // K elements of a stage
   const int kblocks = (int)((p.K + kElems - 1) / kElems);
 
   if (warp == 0) {
-    if (lane == 0) {
-      int kg = 0;
-      for (int i = first; i < total; i += pairs) {
-        int mt, nt;
-        tile_at(i, p.m_tiles, p.n_tiles, mt, nt);
-        const int m0 = mt * 256 + rank * 128;
-        const int n0 = EPI == kEpiGate ? (int)(rank * p.half + nt * 128) : nt * 256 + rank * 128;
-        for (int kb = 0; kb < kblocks; ++kb, ++kg) {
-          const int s = kg % kPS;
-          if (kg >= kPS && !wait(&freeb[s], ((kg / kPS) - 1) & 1)) break;
-          if (*(volatile int *)abort) break;
-          if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * kPStage);
-          const uint32_t bar = map_rank(smem_u32(&full[s]), 0);
+    int kg = 0;
+    bool ok = true;
+    const uint32_t full0 = map_rank(smem_u32(full), 0);
+    for (int i = first; ok && i < total; i += pairs) {
+      const PairItem it = item_at(i, p);
+      const int m0 = it.mt * 256 + rank * 128;
+      const int hw = it.width / 2;   // this CTA's half of the item's B rows
+      const int n0 = EPI == kEpiGate ? (int)(rank * p.half) + it.nt * 128 + it.part * hw
+                                     : it.nt * 256 + it.part * it.width + rank * hw;
+      for (int kb = 0; kb < kblocks; ++kb, ++kg) {
+        const int s = kg % kPS;
+        if (kg >= kPS) ok = wait.warp(&freeb[s], ((kg / kPS) - 1) & 1);
+        if (!ok) break;
+        if (elect_one()) {
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * (kPHalf + hw * 128));
+          const uint32_t bar = full0 + s * 8;
           unsigned char *A = smem + s * kPStage, *B = A + kPHalf;
           const int k0 = kb * kElems;
           if (AMN) {
@@ -179,50 +217,56 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
           }
           if (BMN) {
             tma_load_2d_pair(B, &map_b, n0, k0, bar);
-            tma_load_2d_pair(B + kPHalf / 2, &map_b, n0 + 64, k0, bar);
+            if (hw > 64) tma_load_2d_pair(B + kPHalf / 2, &map_b, n0 + 64, k0, bar);
           } else {
             tma_load_2d_pair(B, &map_b, k0, n0, bar);
+            if (hw > 64) tma_load_2d_pair(B + kPHalf / 2, &map_b, k0, n0 + 64, bar);
           }
         }
-        if (*(volatile int *)abort) break;
+        __syncwarp();
       }
-      // the leader sees both CTAs' copies land; the peer stays until then (cluster_sync)
-      if (rank == 0)
-        for (int t = max(0, kg - kPS); t < kg; ++t) mbar_wait(&full[t % kPS], (t / kPS) & 1);
     }
+    // the leader sees both CTAs' copies land; the peer stays until then (cluster_sync)
+    if (rank == 0)
+      for (int t = max(0, kg - kPS); t < kg; ++t) mbar_wait(&full[t % kPS], (t / kPS) & 1);
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
-      constexpr uint32_t idesc =
-          (KIND == kS8 ? idesc_s8_s32(256, 256) : idesc_bf16_f32(256, 256)) |
-          (AMN ? kIdescMnMajorA : 0) | (BMN ? kIdescMnMajorB : 0);
+    if (rank == 0) {
       int kg = 0, tc = 0;
       for (int i = first; i < total; i += pairs, ++tc) {
         const int acc = tc & 1;
-        if (tc >= 2 && !wait(&accempty[acc], ((tc >> 1) - 1) & 1)) break;
+        if (tc >= 2 && !wait.warp(&accempty[acc], ((tc >> 1) - 1) & 1)) break;
         tc_fence_after();
         const uint32_t d = tmem_base + acc * 256;
+        const int width = item_at(i, p).width;
+        const uint32_t idesc =
+            (KIND == kS8 ? idesc_s8_s32(256, width) : idesc_bf16_f32(256, width)) |
+            (AMN ? kIdescMnMajorA : 0) | (BMN ? kIdescMnMajorB : 0);
         for (int kb = 0; kb < kblocks; ++kb, ++kg) {
           const int s = kg % kPS;
-          const bool ok = wait(&full[s], (kg / kPS) & 1);
+          const bool ok = wait.warp(&full[s], (kg / kPS) & 1);
           tc_fence_after();
-          if (ok) {
-            const uint32_t a = smem_u32(smem + s * kPStage);
-            const uint64_t da = AMN ? smem_desc_mn_sw128(a, kPHalf / 2) : smem_desc_sw128(a);
-            const uint64_t db = BMN ? smem_desc_mn_sw128(a + kPHalf, kPHalf / 2)
-                                    : smem_desc_sw128(a + kPHalf);
+          if (elect_one()) {
+            if (ok) {
+              const uint32_t a = smem_u32(smem + s * kPStage);
+              const uint64_t da = AMN ? smem_desc_mn_sw128(a, kPHalf / 2) : smem_desc_sw128(a);
+              const uint64_t db = BMN ? smem_desc_mn_sw128(a + kPHalf, kPHalf / 2)
+                                      : smem_desc_sw128(a + kPHalf);
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-              // 32 bytes along the rows (K-major), or 16 K rows of 128 bytes (MN-major)
-              const uint64_t ak = da + (AMN ? 128 : 2) * kk, bk = db + (BMN ? 128 : 2) * kk;
-              if (KIND == kS8)
-                umma_s8_pair(d, ak, bk, idesc, kb > 0 || kk > 0);
-              else
-                umma_bf16_pair(d, ak, bk, idesc, kb > 0 || kk > 0);
+              for (int kk = 0; kk < 4; ++kk) {
+                // 32 bytes along the rows (K-major), or 16 K rows of 128 bytes (MN-major)
+                const uint64_t ak = da + (AMN ? 128 : 2) * kk, bk = db + (BMN ? 128 : 2) * kk;
+                if (KIND == kS8)
+                  umma_s8_pair(d, ak, bk, idesc, kb > 0 || kk > 0);
+                else
+                  umma_bf16_pair(d, ak, bk, idesc, kb > 0 || kk > 0);
+              }
             }
+            umma_commit_pair(&freeb[s]);
           }
-          umma_commit_pair(&freeb[s]);
+          __syncwarp();
         }
-        umma_commit_pair(&accfull[acc]);
+        if (elect_one()) umma_commit_pair(&accfull[acc]);
+        __syncwarp();
       }
     }
   } else {
@@ -230,24 +274,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
     unsigned char *buf = smem + kPOut + (warp - 2) * 8192;
     int tc = 0, nst = 0;
     for (int i = first; i < total; i += pairs, ++tc) {
-      int mt, nt;
-      tile_at(i, p.m_tiles, p.n_tiles, mt, nt);
+      const PairItem it = item_at(i, p);
+      const int hw = it.width / 2;
       const int acc = tc & 1;
       if (!wait(&accfull[acc], (tc >> 1) & 1)) break;
       tc_fence_after();
       const uint32_t tb = tmem_base + acc * 256 + ((uint32_t)(q * 32) << 16);
-      const int row0 = mt * 256 + rank * 128 + q * 32;
+      const int row0 = it.mt * 256 + rank * 128 + q * 32;
       const bool rows_in = row0 < p.M;
       if (EPI == kEpiGate) {
-        // columns 0..127 gate, 128..255 up, of the same 128 columns of h
-        for (int c = 0; c < 2; ++c) {
-          const int x = nt * 128 + c * 64;
+        // the first half of the columns is the gate, the second the up projection of the
+        // same columns of h
+        for (int c = 0; c < hw / 64; ++c) {
+          const int x = it.nt * 128 + it.part * hw + c * 64;
           uint32_t hp[32], gp[32], up[32];
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
             uint32_t g[32], u[32];
             tmem_ld32(tb + c * 64 + hf * 32, g);
-            tmem_ld32(tb + 128 + c * 64 + hf * 32, u);
+            tmem_ld32(tb + hw + c * 64 + hf * 32, u);
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
               const float g0 = __uint_as_float(g[2 * k]), g1 = __uint_as_float(g[2 * k + 1]);
@@ -267,8 +312,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
       } else {
         const int row = row0 + lane;
         const float ms = (EPI == kEpiScale && row < p.M) ? __ldg(p.m_scale + row) : 0.f;
-        for (int c = 0; c < 4; ++c) {
-          const int x = nt * 256 + c * 64;
+        for (int c = 0; c < it.width / 64; ++c) {
+          const int x = it.nt * 256 + it.part * it.width + c * 64;
           uint32_t o[32];
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
@@ -569,13 +614,17 @@ int launch_pair(DenseArgs p, DenseOperands o, const CUtensorMap &out, const CUte
   CUtensorMap ta, tb;
   const int64_t brows = EPI == kEpiGate ? 2 * p.half : p.N;
   if (int st = operand_map(&ta, KIND, AMN, o.a, p.M, p.K, 128)) return st;
-  if (int st = operand_map(&tb, KIND, BMN, o.b, brows, p.K, 128)) return st;
+  if (int st = operand_map(&tb, KIND, BMN, o.b, brows, p.K, 64)) return st;
   p.m_tiles = (int)ceil_div(p.M, 256);
   p.n_tiles = (int)ceil_div(p.N, EPI == kEpiGate ? 128 : 256);
   auto k = dense_pair_kernel<KIND, AMN, BMN, EPI, ACT>;
   if (resident_blocks(k, kPThreads, kPSmem) < 0) return NVFP4_ECUDA;
-  const int total = p.m_tiles * p.n_tiles;
-  const int pairs = std::min(total, num_sms() / 2);
+  const int total = p.m_tiles * p.n_tiles, slots = num_sms() / 2;
+  const int left = total % slots;
+  p.cut = left && left * 2 <= slots ? 2 : 1;
+  p.whole = total - left;
+  p.items = p.whole + left * p.cut;
+  const int pairs = std::min(p.items, slots);
   return launch_pdl(k, dim3(2 * pairs), dim3(kPThreads), kPSmem, s, ta, tb, out, g, u, p);
 }
 
