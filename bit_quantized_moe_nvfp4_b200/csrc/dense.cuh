@@ -361,11 +361,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
 }
 
 // ------------------------------------------------------------------ K split over a cluster
-constexpr int kSThreads = 256;   // producer, MMA, 4 TMEM warps; all 8 add and store
+constexpr int kSThreads = 256;   // producer, MMA; all 8 warps read TMEM, add and store
 constexpr int kMaxSplit = 8;     // CTAs of a cluster (the portable limit)
 template <int NT>
 struct SplitShape {
-  static constexpr int kStages = NT == 16 ? 5 : NT == 32 ? 5 : NT == 64 ? 4 : NT == 128 ? 3 : 4;
+  static constexpr int kStages = NT == 16 ? 5 : NT == 32 ? 5 : NT == 64 ? 4 : 3;
   static constexpr uint32_t kA = 128 * 128, kB = NT * 128, kStage = kA + kB;
   // partial tile, fp32 or int32: [NT][128], or [128][NT + 4] for a row-major D
   static constexpr uint32_t kRed = 128 * (NT + 4) * 4;
@@ -374,14 +374,18 @@ struct SplitShape {
   static constexpr uint32_t kMisc = kBars + 8 * (2 * kStages + 1);
   static constexpr uint32_t kSmem = kMisc + 16 + 1024;
   static constexpr uint32_t kTmemCols = NT < 32 ? 32 : NT;
-  // CTAs that share an SM (its 228 KB of shared memory, 1 KB of them reserved for each CTA)
-  static constexpr int kCtas = 2 * (kSmem + 1024) <= 228 * 1024 ? 2 : 1;
+  static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two CTAs an SM (1 KB reserved for each)");
 };
 
-__device__ __forceinline__ float2 ld_cluster_f2(uint32_t addr) {
-  float2 v;
-  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr));
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr));
   return v;
+}
+__device__ __forceinline__ uint2 pack4(float4 v) {
+  return make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
 }
 
 template <int KIND, bool AMN, bool BMN, int EPI, int ACT, int NT>
@@ -497,12 +501,12 @@ __global__ void __launch_bounds__(kSThreads, 2)
   uint32_t *red = reinterpret_cast<uint32_t *>(smem);
   constexpr int kRowPitch = NT + 4;
   const int ncols = (int)min((int64_t)NT, p.N - n0);   // D columns inside the result
-  if (warp >= 4) {
-    const int q = warp & 3, row = q * 32 + lane;
-    const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16);
+  {   // two warps for each quarter of the TMEM lanes, 16 columns at a time in turn
+    const int row = (warp & 3) * 32 + lane;
+    const uint32_t tb = tmem_base + ((uint32_t)((warp & 3) * 32) << 16);
     const bool any = done && kb1 > kb0;
 #pragma unroll 1
-    for (int c = 0; c < ncols; c += 16) {
+    for (int c = (warp >> 2) * 16; c < ncols; c += 32) {
       uint32_t v[16];
       tmem_ld16(tb + c, v);
       if (!any)
@@ -526,65 +530,65 @@ __global__ void __launch_bounds__(kSThreads, 2)
     tmem_dealloc(tmem_base, S::kTmemCols);
   }
   cluster_sync();
-  // Add the cluster's partial tiles: pairs of neighbouring values, this CTA's share of them.
-  const uint32_t base = smem_u32(red);
-  auto sum_at = [&](int at) {   // `at`: index of an even element of the partial tile
-    float2 w[kMaxSplit];
+  // Add the cluster's partial tiles: four neighbouring values a thread, this CTA's share.
+  uint32_t peer[kMaxSplit];
+#pragma unroll
+  for (int r = 0; r < kMaxSplit; ++r) peer[r] = map_rank(smem_u32(red), r < nr ? r : 0);
+  auto sum_at = [&](int at) {   // `at`: index of the first of four elements of the tile
+    float4 w[kMaxSplit];
 #pragma unroll
     for (int r = 0; r < kMaxSplit; ++r)   // all loads first
-      w[r] = r < nr ? ld_cluster_f2(map_rank(base + at * 4, r)) : make_float2(0.f, 0.f);
-    float2 v = make_float2(0.f, 0.f);
-    if (KIND == kS8) {
-      int a = 0, b = 0;
-#pragma unroll
-      for (int r = 0; r < kMaxSplit; ++r) {   // an absent part is 0 in either type
-        a += __float_as_int(w[r].x);
-        b += __float_as_int(w[r].y);
-      }
-      v = make_float2((float)a, (float)b);
-    } else {
+      w[r] = r < nr ? ld_cluster_f4(peer[r] + at * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
+    float4 v = w[0];
+    if (KIND == kS8) {   // an absent part is 0 in either type
+      int a[4] = {0, 0, 0, 0};
 #pragma unroll
       for (int r = 0; r < kMaxSplit; ++r) {
-        v.x += w[r].x;
-        v.y += w[r].y;
+        a[0] += __float_as_int(w[r].x), a[1] += __float_as_int(w[r].y);
+        a[2] += __float_as_int(w[r].z), a[3] += __float_as_int(w[r].w);
       }
+      v = make_float4((float)a[0], (float)a[1], (float)a[2], (float)a[3]);
+    } else {
+#pragma unroll
+      for (int r = 1; r < kMaxSplit; ++r)
+        v.x += w[r].x, v.y += w[r].y, v.z += w[r].z, v.w += w[r].w;
     }
     return v;
   };
+  // M and N are multiples of 8, so four neighbours are all inside or all outside
   if (p.row_major_d) {
-    const int pairs = 128 * (NT / 2);
-    const int e0 = (int)((int64_t)pairs * rank / nr), e1 = (int)((int64_t)pairs * (rank + 1) / nr);
+    const int quads = 128 * (NT / 4);
+    const int e0 = (int)((int64_t)quads * rank / nr), e1 = (int)((int64_t)quads * (rank + 1) / nr);
     for (int e = e0 + (int)threadIdx.x; e < e1; e += kSThreads) {
-      const int m = e / (NT / 2), n = e % (NT / 2) * 2;
-      if (m0 + m < p.M && n0 + n < p.N) {   // N is even
-        const float2 v = sum_at(m * kRowPitch + n);
-        *reinterpret_cast<uint32_t *>(p.out + (int64_t)(m0 + m) * p.ld + n0 + n) =
-            pack_bf16x2(v.x, v.y);
-      }
+      const int m = e / (NT / 4), n = e % (NT / 4) * 4;
+      if (m0 + m < p.M && n0 + n < p.N)
+        *reinterpret_cast<uint2 *>(p.out + (int64_t)(m0 + m) * p.ld + n0 + n) =
+            pack4(sum_at(m * kRowPitch + n));
     }
   } else {
-    const int pairs = ncols * (kTileM / 2);
-    const int e0 = (int)((int64_t)pairs * rank / nr), e1 = (int)((int64_t)pairs * (rank + 1) / nr);
+    const int quads = ncols * (kTileM / 4);
+    const int e0 = (int)((int64_t)quads * rank / nr), e1 = (int)((int64_t)quads * (rank + 1) / nr);
     for (int e = e0 + (int)threadIdx.x; e < e1; e += kSThreads) {
-      const int n = e / (kTileM / 2), m = e % (kTileM / 2) * 2;
-      if (m0 + m >= p.M) continue;   // M is even
-      float2 v = sum_at(n * 128 + m);
+      const int n = e / (kTileM / 4), m = e % (kTileM / 4) * 4;
+      if (m0 + m >= p.M) continue;
+      float4 v = sum_at(n * 128 + m);
       const int64_t row = n0 + n;
       if (EPI == kEpiGate) {
-        const float2 u = sum_at(n * 128 + 64 + m);
+        const float4 u = sum_at(n * 128 + 64 + m);
         if (p.gu) {
-          uint32_t *o = reinterpret_cast<uint32_t *>(p.gu + row * 2 * p.half + m0 + m);
-          o[0] = pack_bf16x2(v.x, v.y);
-          o[p.half / 2] = pack_bf16x2(u.x, u.y);
+          __nv_bfloat16 *o = p.gu + row * 2 * p.half + m0 + m;
+          *reinterpret_cast<uint2 *>(o) = pack4(v);
+          *reinterpret_cast<uint2 *>(o + p.half) = pack4(u);
         }
-        v.x = gate_act<ACT>(v.x) * u.x;
-        v.y = gate_act<ACT>(v.y) * u.y;
+        v.x = gate_act<ACT>(v.x) * u.x, v.y = gate_act<ACT>(v.y) * u.y;
+        v.z = gate_act<ACT>(v.z) * u.z, v.w = gate_act<ACT>(v.w) * u.w;
       } else if (EPI == kEpiScale) {
         const float ts = __ldg(p.n_scale + row);
-        v.x = v.x * ts * __ldg(p.m_scale + m0 + m);
-        v.y = v.y * ts * __ldg(p.m_scale + m0 + m + 1);
+        const float4 ms = __ldg(reinterpret_cast<const float4 *>(p.m_scale + m0 + m));
+        v.x = v.x * ts * ms.x, v.y = v.y * ts * ms.y;
+        v.z = v.z * ts * ms.z, v.w = v.w * ts * ms.w;
       }
-      *reinterpret_cast<uint32_t *>(p.out + row * p.ld + m0 + m) = pack_bf16x2(v.x, v.y);
+      *reinterpret_cast<uint2 *>(p.out + row * p.ld + m0 + m) = pack4(v);
     }
   }
   cluster_sync();   // no CTA leaves while another still reads its partial tile
@@ -644,6 +648,26 @@ int launch_pair(DenseArgs p, DenseOperands o, const CUtensorMap &out, const CUte
   return launch_pdl(k, dim3(2 * pairs), dim3(kPThreads), kPSmem, s, ta, tb, out, g, u, p);
 }
 
+// A kernel of the split kernel's block size whose residency stands for it: the occupancy
+// queries answer one block an SM for kernels that allocate TMEM, whatever they allocate (two
+// run: the split kernel's columns are at most 128 of 512).
+static __global__ void __launch_bounds__(kSThreads, 2) split_shape_kernel() {}
+
+// Over how many CTAs the sum over K is split: as many as keep all clusters resident at once
+// (a second round of clusters costs a whole pass: 8-bit 1 x 6144 x 6144, 48 tiles, 12 us with
+// clusters of 5 of which 56 fit, 16 us with 6 of which 45 fit), one in sixteen left free for
+// the kernel before, which may still be running.  0 after a CUDA error.
+inline int split_count(int64_t tiles, int64_t kblocks, size_t smem) {
+  if (resident_blocks(split_shape_kernel, kSThreads, smem) <= 0) return 0;
+  for (int nr = (int)std::min<int64_t>(kMaxSplit, kblocks); nr > 1; --nr) {
+    const int fit = resident_clusters_fn(reinterpret_cast<const void *>(split_shape_kernel),
+                                         kSThreads, smem, nr);
+    if (fit < 0) return 0;
+    if (tiles * 16 <= (int64_t)fit * 15) return nr;
+  }
+  return 1;
+}
+
 template <int KIND, bool AMN, bool BMN, int EPI, int ACT, int NT>
 int launch_split(DenseArgs p, DenseOperands o, cudaStream_t s) {
   using S = SplitShape<NT>;
@@ -658,9 +682,8 @@ int launch_split(DenseArgs p, DenseOperands o, cudaStream_t s) {
   if (resident_blocks(k, kSThreads, S::kSmem) <= 0) return NVFP4_ECUDA;
   const int64_t tiles = (int64_t)p.m_tiles * p.n_tiles;
   const int64_t kblocks = ceil_div(p.K, KIND == kS8 ? 128 : 64);
-  const int slots = num_sms() * S::kCtas;
-  const int nr = (int)std::max<int64_t>(
-      1, std::min<int64_t>({kMaxSplit, slots / tiles, kblocks}));
+  const int nr = split_count(tiles, kblocks, S::kSmem);
+  if (nr <= 0) return NVFP4_ECUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(tiles * nr));
   cfg.blockDim = dim3(kSThreads);

@@ -76,6 +76,9 @@ int gemm_tile_n();
 // least `smem`); both cached per device.  resident_blocks returns -1 on a CUDA error.
 int num_sms();
 int resident_blocks_fn(const void *fn, int threads, size_t smem);
+// Clusters of `size` blocks of that kernel that the whole device holds at once (the limit must
+// have been raised by resident_blocks before); cached.
+int resident_clusters_fn(const void *fn, int threads, size_t smem, int size);
 template <typename Kern>
 int resident_blocks(Kern k, int threads, size_t smem) {
   return resident_blocks_fn(reinterpret_cast<const void *>(k), threads, smem);

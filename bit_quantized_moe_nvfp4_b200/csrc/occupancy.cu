@@ -74,4 +74,40 @@ int resident_blocks_fn(const void *fn, int threads, size_t smem) {
   return nb;
 }
 
+int resident_clusters_fn(const void *fn, int threads, size_t smem, int size) {
+  struct Entry {
+    const void *fn;
+    int dev, threads, size;
+    size_t smem;
+    int n;
+  };
+  static std::mutex mu;
+  static std::vector<Entry> cache;
+  int dev = 0;
+  cudaGetDevice(&dev);
+  std::lock_guard<std::mutex> lock(mu);
+  for (const Entry &c : cache)
+    if (c.fn == fn && c.dev == dev && c.threads == threads && c.size == size && c.smem == smem)
+      return c.n;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)size);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)size;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  const cudaError_t e = cudaOccupancyMaxActiveClusters(&n, fn, &cfg);
+  if (e != cudaSuccess) {
+    set_last_cuda_error(e);
+    return -1;
+  }
+  if (cache.size() < 1024) cache.push_back({fn, dev, threads, size, smem, n});
+  return n;
+}
+
 }  // namespace nvfp4
