@@ -41,7 +41,7 @@ __device__ __forceinline__ float gate_act(float z) {
 
 struct DenseArgs {
   // Logical product: D[m, n] = sum_k A[m, k] B[n, k].  pair kernel: D rows are the output's
-  // rows.  split kernel: D rows are the output's columns unless `row_major_d`.
+  // rows.  split kernel: D rows are the output's columns, unless ROWS.
   int64_t M, N, K;
   int64_t half;                // kEpiGate: I, the rows of the gate half of w_gu
   const float *m_scale;        // kEpiScale: scale of each D row
@@ -49,7 +49,6 @@ struct DenseArgs {
   __nv_bfloat16 *out;          // split kernel: output, `ld` elements a row
   __nv_bfloat16 *gu;           // split kernel, kEpiGate: [cols, 2 half] pre-activations, or null
   int64_t ld;
-  int row_major_d;             // split kernel: out[m * ld + n] instead of out[n * ld + m]
   int save_gu;                 // pair kernel, kEpiGate: tensor maps g / u are set
   int32_t *flag;               // error bits, or null
   int m_tiles, n_tiles;
@@ -363,17 +362,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
 // ------------------------------------------------------------------ K split over a cluster
 constexpr int kSThreads = 256;   // producer, MMA; all 8 warps read TMEM, add and store
 constexpr int kMaxSplit = 8;     // CTAs of a cluster (the portable limit)
-template <int NT>
+template <int NT, bool ROWS>   // ROWS: the result is row-major in D (out[m][n])
 struct SplitShape {
-  static constexpr int kStages = NT == 16 ? 5 : NT == 32 ? 5 : NT == 64 ? 4 : 3;
+  static constexpr int kStages = NT == 64 ? 4 : 5;
   static constexpr uint32_t kA = 128 * 128, kB = NT * 128, kStage = kA + kB;
-  // partial tile, fp32 or int32: [NT][128], or [128][NT + 4] for a row-major D
-  static constexpr uint32_t kRed = 128 * (NT + 4) * 4;
-  static constexpr uint32_t kRing = kStages * kStage > kRed ? kStages * kStage : kRed;
-  static constexpr uint32_t kBars = (kRing + 15) / 16 * 16;
+  // partial tile, fp32 or int32, in the ring: [NT][128], or [128][NT + 4] (ROWS)
+  static constexpr int kPitch = ROWS ? NT + 4 : 128;
+  static constexpr uint32_t kTile = (ROWS ? 128 : NT) * kPitch * 4;
+  static constexpr uint32_t kBars = kStages * kStage;
   static constexpr uint32_t kMisc = kBars + 8 * (2 * kStages + 1);
   static constexpr uint32_t kSmem = kMisc + 16 + 1024;
   static constexpr uint32_t kTmemCols = NT < 32 ? 32 : NT;
+  static_assert(kTile <= kStages * kStage, "the partial tile fits the ring");
   static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two CTAs an SM (1 KB reserved for each)");
 };
 
@@ -388,11 +388,11 @@ __device__ __forceinline__ uint2 pack4(float4 v) {
   return make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
 }
 
-template <int KIND, bool AMN, bool BMN, int EPI, int ACT, int NT>
+template <int KIND, bool AMN, bool BMN, int EPI, int ACT, int NT, bool ROWS>
 __global__ void __launch_bounds__(kSThreads, 2)
     dense_split_kernel(const __grid_constant__ CUtensorMap map_a,
                        const __grid_constant__ CUtensorMap map_b, DenseArgs p) {
-  using S = SplitShape<NT>;
+  using S = SplitShape<NT, ROWS>;
   extern __shared__ unsigned char smem_raw[];
   unsigned char *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   uint64_t *full = reinterpret_cast<uint64_t *>(smem + S::kBars);
@@ -499,7 +499,6 @@ __global__ void __launch_bounds__(kSThreads, 2)
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   uint32_t *red = reinterpret_cast<uint32_t *>(smem);
-  constexpr int kRowPitch = NT + 4;
   const int ncols = (int)min((int64_t)NT, p.N - n0);   // D columns inside the result
   {   // two warps for each quarter of the TMEM lanes, 16 columns at a time in turn
     const int row = (warp & 3) * 32 + lane;
@@ -512,14 +511,14 @@ __global__ void __launch_bounds__(kSThreads, 2)
       if (!any)
 #pragma unroll
         for (int k = 0; k < 16; ++k) v[k] = 0;
-      if (p.row_major_d) {
+      if (ROWS) {
 #pragma unroll
         for (int k = 0; k < 16; k += 4)
-          *reinterpret_cast<uint4 *>(red + row * kRowPitch + c + k) =
+          *reinterpret_cast<uint4 *>(red + row * S::kPitch + c + k) =
               make_uint4(v[k], v[k + 1], v[k + 2], v[k + 3]);
       } else {
 #pragma unroll
-        for (int k = 0; k < 16; ++k) red[(c + k) * 128 + row] = v[k];
+        for (int k = 0; k < 16; ++k) red[(c + k) * S::kPitch + row] = v[k];
       }
     }
   }
@@ -556,14 +555,14 @@ __global__ void __launch_bounds__(kSThreads, 2)
     return v;
   };
   // M and N are multiples of 8, so four neighbours are all inside or all outside
-  if (p.row_major_d) {
+  if (ROWS) {
     const int quads = 128 * (NT / 4);
     const int e0 = (int)((int64_t)quads * rank / nr), e1 = (int)((int64_t)quads * (rank + 1) / nr);
     for (int e = e0 + (int)threadIdx.x; e < e1; e += kSThreads) {
       const int m = e / (NT / 4), n = e % (NT / 4) * 4;
       if (m0 + m < p.M && n0 + n < p.N)
         *reinterpret_cast<uint2 *>(p.out + (int64_t)(m0 + m) * p.ld + n0 + n) =
-            pack4(sum_at(m * kRowPitch + n));
+            pack4(sum_at(m * S::kPitch + n));
     }
   } else {
     const int quads = ncols * (kTileM / 4);
@@ -571,10 +570,10 @@ __global__ void __launch_bounds__(kSThreads, 2)
     for (int e = e0 + (int)threadIdx.x; e < e1; e += kSThreads) {
       const int n = e / (kTileM / 4), m = e % (kTileM / 4) * 4;
       if (m0 + m >= p.M) continue;
-      float4 v = sum_at(n * 128 + m);
+      float4 v = sum_at(n * S::kPitch + m);
       const int64_t row = n0 + n;
       if (EPI == kEpiGate) {
-        const float4 u = sum_at(n * 128 + 64 + m);
+        const float4 u = sum_at(n * S::kPitch + 64 + m);
         if (p.gu) {
           __nv_bfloat16 *o = p.gu + row * 2 * p.half + m0 + m;
           *reinterpret_cast<uint2 *>(o) = pack4(v);
@@ -617,10 +616,12 @@ inline int out_map(CUtensorMap *m, const void *base, int64_t rows, int64_t cols,
   return st;
 }
 
-// Whether a [rows, cols] result goes to the pair kernel: when its 256 x 256 tiles keep at least
-// half of the CTA pairs busy.
+// Whether a [rows, cols] result goes to the pair kernel: more than 128 rows (half a tile) and
+// tiles enough that, cut in half, they occupy five of eight CTA pairs.  Measured with K = 6144:
+// 24 tiles, 8-bit 256 x 6144: pairs 17 us, split 20; 128 x 6144: pairs 17, split 15; 16 tiles,
+// 8-bit 512 x 2048 x 2048: pairs 9 us, split 8.
 inline bool dense_use_pair(int64_t rows, int64_t cols) {
-  return ceil_div(rows, 256) * ceil_div(cols, 256) * 4 >= num_sms();
+  return rows > 128 && ceil_div(rows, 256) * ceil_div(cols, 256) * 16 >= num_sms() / 2 * 5;
 }
 
 // Where the operands lie: A [M, K] (or [K, M]) and B [N, K] (or [K, N]).
@@ -668,17 +669,16 @@ inline int split_count(int64_t tiles, int64_t kblocks, size_t smem) {
   return 1;
 }
 
-template <int KIND, bool AMN, bool BMN, int EPI, int ACT, int NT>
+template <int KIND, bool AMN, bool BMN, int EPI, int ACT, int NT, bool ROWS = false>
 int launch_split(DenseArgs p, DenseOperands o, cudaStream_t s) {
-  using S = SplitShape<NT>;
-  static_assert(S::kSmem <= 227 * 1024, "shared memory budget");
+  using S = SplitShape<NT, ROWS>;
   CUtensorMap ta, tb;
   const int64_t arows = EPI == kEpiGate ? 2 * p.half : p.M;
   if (int st = operand_map(&ta, KIND, AMN, o.a, arows, p.K, EPI == kEpiGate ? 64 : 128)) return st;
   if (int st = operand_map(&tb, KIND, BMN, o.b, p.N, p.K, NT)) return st;
   p.m_tiles = (int)ceil_div(p.M, EPI == kEpiGate ? 64 : 128);
   p.n_tiles = (int)ceil_div(p.N, NT);
-  auto k = dense_split_kernel<KIND, AMN, BMN, EPI, ACT, NT>;
+  auto k = dense_split_kernel<KIND, AMN, BMN, EPI, ACT, NT, ROWS>;
   if (resident_blocks(k, kSThreads, S::kSmem) <= 0) return NVFP4_ECUDA;
   const int64_t tiles = (int64_t)p.m_tiles * p.n_tiles;
   const int64_t kblocks = ceil_div(p.K, KIND == kS8 ? 128 : 64);
@@ -706,15 +706,15 @@ int launch_split(DenseArgs p, DenseOperands o, cudaStream_t s) {
   return NVFP4_OK;
 }
 
-// The split kernel with the smallest column tile that holds N columns, up to MAXNT.
-template <int KIND, bool AMN, bool BMN, int EPI, int ACT>
+// The split kernel with the smallest column tile that holds N columns, at most 64: at 128 the
+// partial tiles' way through the cluster costs more than the second read of A it saves (8-bit
+// 128 x 4096 x 1024 with its quantizer: 9.8 us against 11.7; it won by 8% at 192..256 x 6144
+// x 4096).
+template <int KIND, bool AMN, int EPI, int ACT>
 int launch_split_n(const DenseArgs &p, DenseOperands o, cudaStream_t s) {
-  if constexpr (!BMN) {
-    if (p.N <= 16) return launch_split<KIND, AMN, BMN, EPI, ACT, 16>(p, o, s);
-    if (p.N <= 32) return launch_split<KIND, AMN, BMN, EPI, ACT, 32>(p, o, s);
-    if (p.N <= 64) return launch_split<KIND, AMN, BMN, EPI, ACT, 64>(p, o, s);
-  }
-  return launch_split<KIND, AMN, BMN, EPI, ACT, 128>(p, o, s);
+  if (p.N <= 16) return launch_split<KIND, AMN, false, EPI, ACT, 16>(p, o, s);
+  if (p.N <= 32) return launch_split<KIND, AMN, false, EPI, ACT, 32>(p, o, s);
+  return launch_split<KIND, AMN, false, EPI, ACT, 64>(p, o, s);
 }
 
 }  // namespace nvfp4

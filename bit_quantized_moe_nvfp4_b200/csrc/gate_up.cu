@@ -79,7 +79,7 @@ int forward(const __nv_bfloat16 *x, const __nv_bfloat16 *w_gu, int64_t T, int64_
     return launch_pair<kBf16, false, false, kEpiGate, ACT>(p, {x, w_gu}, th, tg, tu, s);
   }
   p.M = I, p.N = T;
-  return launch_split_n<kBf16, false, false, kEpiGate, ACT>(p, {w_gu, x}, s);
+  return launch_split_n<kBf16, false, kEpiGate, ACT>(p, {w_gu, x}, s);
 }
 
 int check(int64_t T, int64_t H, int64_t I, int act) {
@@ -155,7 +155,7 @@ extern "C" int moe_nvfp4_gate_up_backward(const __nv_bfloat16 *dh, const __nv_bf
         return st;
     } else {
       p.M = H, p.N = T;
-      if (int st = launch_split_n<kBf16, true, false, kEpiStore, 0>(p, {w_gu, dgu}, stream))
+      if (int st = launch_split_n<kBf16, true, kEpiStore, 0>(p, {w_gu, dgu}, stream))
         return st;
     }
   }
@@ -166,8 +166,7 @@ extern "C" int moe_nvfp4_gate_up_backward(const __nv_bfloat16 *dh, const __nv_bf
       if (int st = out_map(&to, dw_gu, 2 * I, H, H)) return st;
       return launch_pair<kBf16, true, true, kEpiStore, 0>(p, {dgu, x}, to, to, to, stream);
     }
-    p.row_major_d = 1;
-    return launch_split_n<kBf16, true, true, kEpiStore, 0>(p, {dgu, x}, stream);
+    return launch_split<kBf16, true, true, kEpiStore, 0, 64, true>(p, {dgu, x}, stream);
   }
   return NVFP4_OK;
 }

@@ -36,5 +36,5 @@ extern "C" int nvfp4_int8_matmul(const int8_t *a, const float *a_scales, const i
     return launch_pair<kS8, false, false, kEpiScale, 0>(p, {a, w}, to, to, to, stream);
   }
   p.M = N, p.N = T, p.m_scale = w_scales, p.n_scale = a_scales;
-  return launch_split_n<kS8, false, false, kEpiScale, 0>(p, {w, a}, stream);
+  return launch_split_n<kS8, false, kEpiScale, 0>(p, {w, a}, stream);
 }
