@@ -570,6 +570,11 @@ def moe_nvfp4_forward_static(x, topk_ids, topk_w, w_gu, s_gu, g_gu, w_dn, s_dn, 
 # ------------------------------------------------------------------------------ dense operators
 # One token's call is shorter on the GPU than in Python, so these helpers do little: the raw
 # stream handle instead of a Stream object (2 us less a call), one attribute test each.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",   # absent without CUDA
+                      lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def _arg(t, dtype, shape, dev: int, name: str):
     """Address of a contiguous tensor of this type and shape on CUDA device `dev`."""
     try:
@@ -588,18 +593,22 @@ def _optional(t, dtype, shape, dev: int, name: str):
 
 def _out(t, like, dtype, shape, dev: int, name: str):
     """(`t`, or a new tensor beside `like`; its address)."""
-    if t is None:
+    if t is not None:
+        return t, _arg(t, dtype, shape, dev, name)
+    if like.shape != shape:
         t = torch.empty(*shape, dtype=dtype, device=like.device)
-        return t, t.data_ptr()
-    return t, _arg(t, dtype, shape, dev, name)
+    else:   # empty_like is the quicker of the two, and quicker still without a dtype
+        t = torch.empty_like(like) if like.dtype is dtype else torch.empty_like(like, dtype=dtype)
+    return t, t.data_ptr()
 
 
 def _rows(x, name: str):
     """(T, H, device index) of a two-dimensional tensor."""
-    if not isinstance(x, torch.Tensor) or x.dim() != 2:
-        raise ValueError(f"{name}: expected a two-dimensional tensor")
-    T, H = x.shape
-    return T, H, x.get_device()
+    try:
+        T, H = x.shape
+        return T, H, x.get_device()
+    except (AttributeError, ValueError):
+        raise ValueError(f"{name}: expected a two-dimensional tensor") from None
 
 
 def _scratch(workspace, nbytes: int, like):
@@ -616,11 +625,11 @@ def _scratch(workspace, nbytes: int, like):
 def _run(name: str, dev: int, *args) -> None:
     """Call an entry point on CUDA device `dev` and that device's current stream."""
     f = getattr(_LIB or _lib(), name)
-    if dev == torch._C._cuda_getDevice():
-        status = f(*args, torch._C._cuda_getCurrentRawStream(dev))
+    if dev == _current_device():
+        status = f(*args, _raw_stream(dev))
     else:
         with torch.cuda.device(dev):
-            status = f(*args, torch._C._cuda_getCurrentRawStream(dev))
+            status = f(*args, _raw_stream(dev))
     if status:
         _check(status)
 
@@ -698,14 +707,14 @@ def moe_nvfp4_pre_norm_backward(dy, x, weight, eps: float, dskip=None, dx=None, 
     pw = _arg(weight, bf, (H,), dev, "weight")
     ps = _optional(dskip, bf, (T, H), dev, "dskip")
     dx, pdx = _out(dx, x, bf, (T, H), dev, "dx")
-    dweight, pdw = _out(dweight, x, bf, (H,), dev, "dweight")
+    dweight, pdw = _out(dweight, weight, bf, (H,), dev, "dweight")
     workspace, pws, nws = _scratch(workspace, _norm_scratch(T, H, dev), x)
     _run("moe_nvfp4_pre_norm_backward", dev, pd, px, pw, ps, T, H, eps, pdx, pdw, pws, nws)
     return dx, dweight
 
 
 def _norm_scratch(T, H, dev):
-    if dev == torch._C._cuda_getDevice():
+    if dev == _current_device():
         return _lib().moe_nvfp4_norm_backward_workspace_size(T, H)
     with torch.cuda.device(dev):
         return _lib().moe_nvfp4_norm_backward_workspace_size(T, H)
@@ -724,10 +733,10 @@ def moe_nvfp4_post_norm_backward(dout, y, weight, eps: float, gate=None,
     pw = _arg(weight, bf, (H,), dev, "weight")
     pg, rows, cols = _gate(gate, T, H, dev)
     dy, pdy = _out(dy, y, bf, (T, H), dev, "dy")
-    dweight, pdw = _out(dweight, y, bf, (H,), dev, "dweight")
+    dweight, pdw = _out(dweight, weight, bf, (H,), dev, "dweight")
     pdg = pdr = None
     if gate is not None:
-        dgate, pdg = _out(dgate, y, bf, (rows, cols), dev, "dgate")
+        dgate, pdg = _out(dgate, gate, bf, (rows, cols), dev, "dgate")
     elif dgate is not None:
         raise ValueError("dgate needs gate")
     if need_dresidual or dresidual is not None:
@@ -774,7 +783,7 @@ def moe_nvfp4_gate_up_backward(dh, x, w_gu, gu, act: int = ACT_SILU, dx=None, dw
     if need_dx or dx is not None:
         dx, pdx = _out(dx, x, bf, (T, H), dev, "dx")
     if need_dw or dw_gu is not None:
-        dw_gu, pdw = _out(dw_gu, x, bf, (2 * I, H), dev, "dw_gu")
+        dw_gu, pdw = _out(dw_gu, w_gu, bf, (2 * I, H), dev, "dw_gu")
     workspace, pws, nws = _scratch(workspace, moe_nvfp4_gate_up_backward_workspace_size(T, I), x)
     _run("moe_nvfp4_gate_up_backward", dev, pd, px, pw, pgu, T, H, I, act, pdx, pdw, pws, nws,
          _flag(error_flag, dev))

@@ -85,7 +85,9 @@ int forward(const __nv_bfloat16 *x, const __nv_bfloat16 *w_gu, int64_t T, int64_
 int check(int64_t T, int64_t H, int64_t I, int act) {
   if (T < 0 || H <= 0 || I <= 0 || (act != NVFP4_ACT_SILU && act != NVFP4_ACT_GELU))
     return NVFP4_EINVAL;
-  if (H % 8 || I % 8 || H > 65536 || I > 65536 || T >= (int64_t(1) << 30)) return NVFP4_ESHAPE;
+  if (H % 8 || I % 8 || H > 65536 || I > 65536 || T >= (int64_t(1) << 30) ||
+      T > (int64_t(1) << 44) / std::max(H, 2 * I))
+    return NVFP4_ESHAPE;
   return NVFP4_OK;
 }
 

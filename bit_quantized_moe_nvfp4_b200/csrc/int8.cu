@@ -19,7 +19,9 @@ extern "C" int nvfp4_int8_matmul(const int8_t *a, const float *a_scales, const i
                                  const float *w_scales, int64_t T, int64_t N, int64_t K,
                                  __nv_bfloat16 *out, int32_t *error_flag, cudaStream_t stream) {
   if (T < 0 || N <= 0 || K <= 0) return NVFP4_EINVAL;
-  if (K % 16 || N % 8 || K > 32768 || N > (1 << 24) || T >= (int64_t(1) << 30)) return NVFP4_ESHAPE;
+  if (K % 16 || N % 8 || K > 32768 || N > (1 << 24) || T >= (int64_t(1) << 30) ||
+      T > (int64_t(1) << 44) / N)
+    return NVFP4_ESHAPE;
   if (!w || !w_scales || !aligned16(w) || !aligned16(w_scales) ||
       (reinterpret_cast<uintptr_t>(error_flag) & 3))
     return NVFP4_EINVAL;

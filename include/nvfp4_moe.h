@@ -462,8 +462,8 @@ NVFP4_API int moe_nvfp4_post_norm_backward(
  * error_flag: [1] int32, device, may be NULL: bit 1 is ORed in if a device-side wait gave up
  * (the outputs are then invalid); nothing else is written, so the caller zeroes it once.
  * No workspace.  T == 0 enqueues nothing.
- * Limits: H % 8 == 0, I % 8 == 0, H and I <= 65536, T < 2^30.  Alignment: 16 bytes
- * (error_flag 4).  Outputs must not overlap inputs.  Errors: EINVAL, ESHAPE, ECUDA. */
+ * Limits: H % 8 == 0, I % 8 == 0, H and I <= 65536, T < 2^30, T max(H, 2I) <= 2^44.
+ * Alignment: 16 bytes (error_flag 4).  Outputs must not overlap inputs.  Errors: EINVAL, ESHAPE, ECUDA. */
 NVFP4_API int moe_nvfp4_gate_up(const __nv_bfloat16 *x, const __nv_bfloat16 *w_gu, int64_t T,
                                 int64_t H, int64_t I, int act, __nv_bfloat16 *h,
                                 __nv_bfloat16 *gu, int32_t *error_flag, cudaStream_t stream);
@@ -501,8 +501,8 @@ NVFP4_API int nvfp4_int8_quantize(const __nv_bfloat16 *x, int64_t rows, int64_t 
 /* out[t, n] = bf16( (sum_k a[t, k] w[n, k]) a_scales[t] w_scales[n] ): exact int32 sums.
  *   a [T, K] int8   a_scales [T] fp32   w [N, K] int8   w_scales [N] fp32   out [T, N] bf16
  * error_flag as in moe_nvfp4_gate_up.  No workspace.  T == 0 enqueues nothing.
- * Limits: K % 16 == 0, K <= 32768, N % 8 == 0, N <= 2^24, T < 2^30.  Alignment: a, w,
- * w_scales and out 16 bytes, a_scales and error_flag 4.  Errors: EINVAL, ESHAPE, ECUDA. */
+ * Limits: K % 16 == 0, K <= 32768, N % 8 == 0, N <= 2^24, T < 2^30, T N <= 2^44.  Alignment:
+ * a, w, w_scales and out 16 bytes, a_scales and error_flag 4.  Errors: EINVAL, ESHAPE, ECUDA. */
 NVFP4_API int nvfp4_int8_matmul(const int8_t *a, const float *a_scales, const int8_t *w,
                                 const float *w_scales, int64_t T, int64_t N, int64_t K,
                                 __nv_bfloat16 *out, int32_t *error_flag, cudaStream_t stream);

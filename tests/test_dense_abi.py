@@ -100,7 +100,8 @@ def test_gate_up(lib):
                 dict(act=2), dict(act=-1), dict(x=OK + 2), dict(w=OK + 2), dict(h=OK + 2),
                 dict(gu=OK + 2), dict(flag=OK + 2)):
         assert fwd(**bad) == -1, bad
-    for bad in (dict(H=60), dict(I=12), dict(H=65544), dict(I=65544), dict(T=1 << 30)):
+    for bad in (dict(H=60), dict(I=12), dict(H=65544), dict(I=65544), dict(T=1 << 30),
+                dict(T=(1 << 28) + 1, I=32768)):
         assert fwd(**bad) == -2, bad
     size = lib.moe_nvfp4_gate_up_backward_workspace_size
     size.restype, size.argtypes = SZ, [I64, I64]
@@ -125,7 +126,8 @@ def test_int8_matmul(lib):
                 dict(T=-1), dict(N=0), dict(K=0), dict(a=OK + 8), dict(w=OK + 8), dict(sw=OK + 4),
                 dict(sa=OK + 2), dict(out=OK + 2), dict(flag=OK + 2)):
         assert call(**bad) == -1, bad
-    for bad in (dict(K=72), dict(N=12), dict(K=32784), dict(N=(1 << 24) + 8), dict(T=1 << 30)):
+    for bad in (dict(K=72), dict(N=12), dict(K=32784), dict(N=(1 << 24) + 8), dict(T=1 << 30),
+                dict(T=(1 << 24), N=(1 << 20) + 8)):
         assert call(**bad) == -2, bad
 
 

@@ -49,11 +49,13 @@ def inputs(T, H, I):
     return draw(T + H, T, H), draw(I + H, 2 * I, H, std=H ** -0.5)
 
 
-# T up to 16, 32, 64, 128 and above: each column tile of the split kernel; many rows and
-# columns: pairs of CTAs.  Sizes that end inside every tile.
+# T up to 16, 32 and above: each column tile of the split kernel.  Many rows and columns: pairs of
+# CTAs, with tiles cut in half (34, 36 tiles), whole ones only (72), a whole round and a cut one
+# (90), and four rounds (289), where accumulators and stages are used again.  Sizes that end
+# inside every tile.
 SHAPES = [(1, 64, 8), (2, 200, 72), (16, 264, 64), (17, 136, 200), (33, 64, 136), (64, 512, 64),
           (65, 72, 328), (129, 264, 520), (300, 128, 8), (257, 192, 2056), (1000, 520, 1032),
-          (2049, 64, 1024)]
+          (2049, 64, 1024), (2500, 72, 1032), (4100, 136, 2056)]
 
 
 @pytest.mark.parametrize("T,H,I", SHAPES)
@@ -83,7 +85,8 @@ def dgu_ref(gu, dh, act):
     return d
 
 
-@pytest.mark.parametrize("T,H,I", SHAPES + [(4096, 256, 64), (40, 2048, 1032)])
+@pytest.mark.parametrize("T,H,I", SHAPES + [(4096, 256, 64), (40, 2048, 1032), (1100, 1544, 72),
+                                           (4100, 4104, 72)])
 @pytest.mark.parametrize("act", [0, 1], ids=["silu", "gelu"])
 def test_gate_up_backward(nv, T, H, I, act):
     x, w = (t.cuda() for t in inputs(T, H, I))
@@ -180,6 +183,20 @@ def test_outputs_end_where_they_end(nv):
         nv.moe_nvfp4_gate_up_backward(buf[:T], x.cuda(), w.cuda(), gbuf[:T], dx=dxb[:T],
                                       dw_gu=dwb[:2 * I])
         assert (dxb[T:] == 7).all() and (dwb[2 * I:] == 7).all()
+
+
+def test_results_beyond_32_bit_offsets(nv):
+    """h and gu of more than 2^31 elements: the first, middle and last rows are right."""
+    T, H, I = 140000, 8, 8192
+    x, w = draw(1, T, H), draw(2, 2 * I, H, std=0.5)
+    gu = torch.empty(T, 2 * I, dtype=torch.bfloat16, device="cuda")
+    h = nv.moe_nvfp4_gate_up(x.cuda(), w.cuda(), gu=gu)
+    for t in (0, 131071, 131072, T - 1):
+        ref = x[t].double() @ w.double().t()
+        mag = x[t].double().abs() @ w.double().abs().t() * (H * U)
+        close(gu[t], ref, mag)
+        g, u, e = ref[:I], ref[I:], 1.13 * mag[:I] + 2.0 ** -19 * (1 + ref[:I].abs())
+        close(h[t], act_fn(0, g) * u, e * u.abs() + act_fn(0, g).abs() * mag[I:] + e * mag[I:])
 
 
 def test_zero_tokens(nv):

@@ -30,7 +30,7 @@ def case(T, N, K, seed=0, full=False):
 
 SHAPES = [(1, 8, 16), (1, 1000, 784), (2, 72, 2064), (16, 136, 128), (17, 264, 400), (33, 64, 128),
           (65, 328, 272), (129, 1000, 528), (300, 8, 16), (257, 2056, 336), (1000, 2064, 1040),
-          (2049, 1032, 64), (4, 256, 32768)]
+          (2049, 1032, 64), (4, 256, 32768), (2500, 2056, 144), (4100, 4104, 272)]
 
 
 @pytest.mark.parametrize("T,N,K", SHAPES)
@@ -67,6 +67,15 @@ def test_output_ends_where_it_ends(nv):
         buf = torch.full((T + 8, N), 7.0, dtype=torch.bfloat16, device="cuda")
         nv.nvfp4_int8_matmul(a, sa, w, sw, out=buf[:T])
         assert (buf[T:] == 7).all()
+
+
+def test_results_beyond_32_bit_offsets(nv):
+    T, N, K = 262200, 8200, 16
+    a, sa, w, sw = case(T, N, K)
+    out = nv.nvfp4_int8_matmul(a.cuda(), sa.cuda(), w.cuda(), sw.cuda())
+    for t in (0, 131072, 261889, T - 1):
+        ref = (a[t].double() @ w.double().t()) * sa[t].double() * sw.double()
+        assert ((out[t].cpu().double() - ref).abs() <= (B + 2.0 ** -22) * ref.abs()).all()
 
 
 def test_zero_tokens(nv):

@@ -231,6 +231,21 @@ def test_rows_do_not_touch_each_other(nv):
         assert torch.equal(bc[t], cc[t]) and bs[t] == cs[t]
 
 
+def test_rows_beyond_32_bit_offsets(nv):
+    T, H = 350000, 6144
+    x = torch.empty(T, H, dtype=torch.bfloat16, device="cuda").fill_(1.0)
+    w = draw(2, H, std=0.1, mean=1.0)
+    rows = [0, 174762, 174763, 349525, T - 1]
+    x[rows] = draw(1, len(rows), H).cuda()
+    out = nv.moe_nvfp4_pre_norm(x, w.cuda(), EPS)
+    xd = x[rows].cpu().double()
+    ref = w.double() * xd * rms(xd)
+    close(out[rows], ref, E * ref.abs())
+    dx, _ = nv.moe_nvfp4_pre_norm_backward(out, x, w.cuda(), EPS)
+    dr, drm, *_ = grads(x[rows].cpu(), w, None, out[rows].cpu(), 1.0)
+    close(dx[rows], dr, E * drm)
+
+
 def test_zero_rows(nv):
     H = 264
     x, w = torch.empty(0, H, dtype=torch.bfloat16).cuda(), draw(1, H).cuda()
