@@ -27,7 +27,7 @@ namespace {
 
 constexpr int64_t kMaxH = 32768;   // 4 vectors of 8 values for each of 1024 threads
 constexpr int kWarpRowVecs = 192;  // rows of up to 192 vectors (1536 values) take a warp
-constexpr int kWarps = 4;          // warps of a CTA whose warps take a row each
+constexpr int kWarps = 8;          // warps of a CTA whose warps take a row each
 
 enum { kPre = 0, kPreInt8 = 1, kPost = 2, kPostNext = 3, kQuant = 4 };
 
@@ -163,14 +163,16 @@ __device__ __forceinline__ float code_scale(float amax) {
   return amax > 0.f ? __fdiv_rn(amax, 127.f) : 1.f;
 }
 
-// CTAs that an SM holds: registers and shared memory are shared out for so
-// many.  Three against two or four: post_norm with next of 16384 x 6144, 140 us against 161
+// CTAs that an SM holds: registers and shared memory are shared out for so many.  Of 256
+// threads three, against two or four: post_norm with next of 16384 x 6144, 140 us against 161
 // and 144; gradients of 4096 x 6144, 45 us against 52 (with a channel gate's column sums in
-// registers too, or four vectors a thread, two fit).
-constexpr int row_ctas(int maxt) { return maxt == 1024 ? 1 : maxt ? 3 : 6; }
+// registers too, or four vectors a thread, two fit).  Gradients of short rows: the fewer CTAs
+// the fewer partial sums to add (forward and backward of 8191 x 1032: 30.7 us with 2 CTAs of 8
+// warps, 33.3 with 4 of 4).
+constexpr int row_ctas(int maxt) { return maxt == 1024 ? 1 : 3; }
 constexpr int grad_row_ctas(int maxt, int vpt, bool sum_g) {
   if (maxt == 1024) return 1;
-  if (!maxt) return vpt <= 4 || !sum_g ? 4 : 3;
+  if (!maxt) return vpt <= 2 && !sum_g ? 3 : 2;
   return vpt == 1 ? 4 : vpt == 4 || (vpt == 3 && sum_g) ? 2 : 3;
 }
 
@@ -520,33 +522,38 @@ __global__ void __launch_bounds__(max_threads<MAXT>(), grad_row_ctas(MAXT, VPT, 
   }
   // this CTA's sums, always in the same order
   if (WARP) {
-    float *acc_s = reinterpret_cast<float *>(dyn_smem);   // [2][H]; the slots are empty
+    // each warp's sums as [i][j][lane] pairs in the slots, which are empty now, then their total
+    constexpr int kPart = VPT * 4 * 32;   // pairs of one warp
+    float2 *acc = reinterpret_cast<float2 *>(dyn_smem);
     const int warp = threadIdx.x >> 5;
     cp_async_wait(0);
     __syncthreads();
-    for (int w = 0; w < kWarps; ++w) {
-      if (warp == w) {
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-          const int c = me + i * 32;
-          if (c >= nvec) continue;
+    for (int i = 0; i < VPT; ++i)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            float2 *at = reinterpret_cast<float2 *>(acc_s + c * 8 + 2 * j);
-            *at = w ? add2(*at, aw[i][j]) : aw[i][j];
-            at = reinterpret_cast<float2 *>(acc_s + p.H + c * 8 + 2 * j);
-            if (SUMG) *at = w ? add2(*at, ag[i][j]) : ag[i][j];
-          }
-        }
-        if (me == 0) buf[0] = w ? buf[0] + a1 : a1;
+      for (int j = 0; j < 4; ++j) {
+        acc[warp * kPart + (i * 4 + j) * 32 + me] = aw[i][j];
+        if (SUMG) acc[(kWarps + warp) * kPart + (i * 4 + j) * 32 + me] = ag[i][j];
       }
-      __syncthreads();
+    if (me == 0) buf[warp] = a1;
+    __syncthreads();
+    for (int e = threadIdx.x; e < kPart; e += blockDim.x) {
+      const int at = ((e >> 7) * 32 + (e & 31)) * 8 + ((e >> 5) & 3) * 2;   // column of the pair
+      if (at >= p.H) continue;
+#pragma unroll
+      for (int k = 0; k < (SUMG ? 2 : 1); ++k) {
+        float2 v = acc[k * kWarps * kPart + e];
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) v = add2(v, acc[(k * kWarps + w) * kPart + e]);
+        *reinterpret_cast<float2 *>((k ? p.part_g : p.part_w) + (int64_t)blockIdx.x * p.H + at) = v;
+      }
     }
-    for (int c = threadIdx.x; c < p.H; c += blockDim.x) {
-      p.part_w[(int64_t)blockIdx.x * p.H + c] = acc_s[c];
-      if (SUMG) p.part_g[(int64_t)blockIdx.x * p.H + c] = acc_s[p.H + c];
+    if (p.sum_g == 2 && threadIdx.x == 0) {
+      float v = buf[0];
+#pragma unroll
+      for (int w = 1; w < kWarps; ++w) v += buf[w];
+      p.part_g[blockIdx.x] = v;
     }
-    if (p.sum_g == 2 && threadIdx.x == 0) p.part_g[blockIdx.x] = buf[0];
   } else {
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
@@ -689,7 +696,8 @@ int run_grad(NormGradParams &p, RowArrays rows, __nv_bfloat16 *dw, __nv_bfloat16
   p.part_g = reinterpret_cast<float *>(static_cast<char *>(ws) + align256((size_t)most * p.H * 4));
   const RowShape rs = row_shape(p.H / 8, p.T < num_sms());
   size_t smem = plan_rows(&rows, rs, grad_row_ctas(rs.maxt, rs.vpt, p.sum_g == 1));
-  if (!rs.maxt) smem = std::max(smem, (size_t)p.H * 8);   // the warps' sums of dweight and dgate
+  if (!rs.maxt)   // the warps' sums of dweight, and of a channel gate's gradient
+    smem = std::max(smem, (size_t)(p.sum_g == 1 ? 2 : 1) * kWarps * rs.vpt * 4 * 32 * 8);
   auto launch = [&](auto k) {
     const int nb = resident_blocks(k, rs.threads, smem);
     if (nb <= 0) return (int)NVFP4_ECUDA;
