@@ -398,9 +398,11 @@ NVFP4_API int moe_nvfp4_forward_w4a4_profiled(
  *   eps      > 0 (an all-zero row gives zeros)
  *   gate     [gate_rows, gate_cols] bf16 with gate_rows 1 or T and gate_cols 1 or H,
  *            broadcast over [T, H]; or NULL with gate_rows = gate_cols = 0 for no gate
- * T == 0 enqueues nothing (a gradient summed over tokens is set to zero).  Outputs must not
- * overlap inputs or one another.  Infinite or NaN values stay in their own row, except in the
- * gradients that are summed over rows.
+ * T == 0 enqueues nothing (a gradient summed over tokens is set to zero).  A row is read
+ * before it is written, so an output may be the very tensor of an input of its type and shape
+ * (the residual stream in place); no other overlap is allowed.  Infinite or NaN values stay in
+ * their own row, except in the gradients that are summed over rows.  A row whose sum of squares
+ * exceeds fp32 counts as infinitely long: its norm is 0.
  * Limits: H % 8 == 0, H <= 32768 (pre_norm_int8: H % 16 == 0).
  * Alignment: 16 bytes; a gate with gate_cols 1, and its gradient, 2 bytes; scales 4 bytes.
  * Errors: EINVAL, ESHAPE, EWORKSPACE (backward), ECUDA.
@@ -431,8 +433,8 @@ NVFP4_API int moe_nvfp4_post_norm(const __nv_bfloat16 *y, const __nv_bfloat16 *w
  *   post_norm:  as above with dout gate in the place of dy;  dresidual = residual_scale dout
  *               (NULL: not wanted);  dgate = dout weight n summed over the axes along which
  *               gate is broadcast, [gate_rows, gate_cols] (NULL exactly when gate is)
- * Sums over tokens are taken in an order that the sizes fix: equal calls on one kind of device
- * give equal bits.  Workspace: moe_nvfp4_norm_backward_workspace_size bytes, 16-byte aligned,
+ * Sums over tokens are taken in an order that sizes and device fix: equal calls give equal
+ * bits.  Workspace: moe_nvfp4_norm_backward_workspace_size bytes, 16-byte aligned,
  * no initialisation; calls that share one must not overlap in time. */
 NVFP4_API size_t moe_nvfp4_norm_backward_workspace_size(int64_t T, int64_t H);
 NVFP4_API int moe_nvfp4_pre_norm_backward(const __nv_bfloat16 *dy, const __nv_bfloat16 *x,
@@ -472,7 +474,7 @@ NVFP4_API int moe_nvfp4_gate_up(const __nv_bfloat16 *x, const __nv_bfloat16 *w_g
  *   dg = bf16( dh u act'(g) ),  du = bf16( dh act(g) )      into the workspace
  *   dx    = bf16( [dg | du] w_gu )      [T, H], or NULL: not wanted (w_gu may then be NULL)
  *   dw_gu = bf16( [dg | du]^T x )       [2I, H], or NULL: not wanted (x may then be NULL)
- * with fp32 sums whose order the sizes fix.  T == 0 sets dw_gu to zero.
+ * with fp32 sums whose order sizes and device fix.  T == 0 sets dw_gu to zero.
  * Workspace: moe_nvfp4_gate_up_backward_workspace_size bytes, 16-byte aligned, no
  * initialisation.  Limits, alignment and error_flag as moe_nvfp4_gate_up.
  * Errors: EINVAL (also dx and dw_gu both NULL), ESHAPE, EWORKSPACE, ECUDA. */

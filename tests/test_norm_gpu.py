@@ -214,6 +214,29 @@ def test_gradients_against_differences(nv):
         assert abs(diff - float((gr * e).sum())) <= tol
 
 
+@pytest.mark.parametrize("T,H", [(3, 264), (700, 6144), (900, 1032)])
+def test_in_place(nv, T, H):
+    """An output that is an input's own tensor."""
+    y, res, w = draw(1, T, H).cuda(), draw(2, T, H).cuda(), draw(3, H, std=0.1, mean=1.0).cuda()
+    g, d = draw(4, T, H).cuda(), draw(5, T, H).cuda()
+    want = nv.moe_nvfp4_post_norm(y, w, res, EPS, gate=g, next_weight=w)
+    a, b = res.clone(), y.clone()
+    nv.moe_nvfp4_post_norm(b, w, a, EPS, gate=g, next_weight=w, out=a, next_out=b)
+    assert torch.equal(a, want[0]) and torch.equal(b, want[1])
+    a = y.clone()
+    assert torch.equal(nv.moe_nvfp4_pre_norm(a, w, EPS, out=a), nv.moe_nvfp4_pre_norm(y, w, EPS))
+    want = nv.moe_nvfp4_pre_norm_backward(d, y, w, EPS, dskip=res)
+    for k in range(3):
+        args = [d.clone(), y.clone(), res.clone()]
+        got = nv.moe_nvfp4_pre_norm_backward(args[0], args[1], w, EPS, dskip=args[2], dx=args[k])
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    want = nv.moe_nvfp4_post_norm_backward(d, y, w, EPS, gate=g, residual_scale=0.5)
+    a, b, c = d.clone(), y.clone(), g.clone()
+    got = nv.moe_nvfp4_post_norm_backward(a, b, w, EPS, gate=c, residual_scale=0.5, dy=b,
+                                          dgate=c, dresidual=a)
+    assert all(torch.equal(p, q) for p, q in zip(got, want))
+
+
 def test_rows_do_not_touch_each_other(nv):
     """NaN and infinity in one row leave the others as they are; a row of zeros gives zeros."""
     T, H = 6, 264
