@@ -602,13 +602,24 @@ def _out(t, like, dtype, shape, dev: int, name: str):
     return t, t.data_ptr()
 
 
-def _rows(x, name: str):
-    """(T, H, device index) of a two-dimensional tensor."""
+def _matrix(x, dtype, name: str):
+    """(rows, columns, device index, address) of a contiguous two-dimensional CUDA tensor."""
     try:
         T, H = x.shape
-        return T, H, x.get_device()
+        dev = x.get_device()
+        if x.dtype is dtype and dev >= 0 and x.is_contiguous():
+            return T, H, dev, x.data_ptr()
     except (AttributeError, ValueError):
-        raise ValueError(f"{name}: expected a two-dimensional tensor") from None
+        pass
+    raise ValueError(f"{name}: expected a contiguous two-dimensional CUDA tensor of {dtype}")
+
+
+def _weight(w, dtype, cols: int, dev: int, name: str):
+    """(rows, address) of a matrix with `cols` columns on device `dev`."""
+    rows, n, where, address = _matrix(w, dtype, name)
+    if n != cols or where != dev:
+        raise ValueError(f"{name}: expected rows of {cols} values on cuda:{dev}")
+    return rows, address
 
 
 def _scratch(workspace, nbytes: int, like):
@@ -640,8 +651,7 @@ def _flag(error_flag, dev: int):
 
 def moe_nvfp4_pre_norm(x, weight, eps: float, out=None) -> torch.Tensor:
     """weight * x / sqrt(mean(x^2) + eps) for each row of x bf16 [T, H]; weight bf16 [H]."""
-    T, H, dev = _rows(x, "x")
-    px = _arg(x, torch.bfloat16, (T, H), dev, "x")
+    T, H, dev, px = _matrix(x, torch.bfloat16, "x")
     pw = _arg(weight, torch.bfloat16, (H,), dev, "weight")
     out, po = _out(out, x, torch.bfloat16, (T, H), dev, "out")
     _run("moe_nvfp4_pre_norm", dev, px, pw, T, H, eps, po)
@@ -651,8 +661,7 @@ def moe_nvfp4_pre_norm(x, weight, eps: float, out=None) -> torch.Tensor:
 def moe_nvfp4_pre_norm_int8(x, weight, eps: float, codes=None, scales=None):
     """moe_nvfp4_pre_norm's rows as 8-bit codes and one scale each, for nvfp4_int8_matmul.
     Returns (codes int8 [T, H], scales fp32 [T])."""
-    T, H, dev = _rows(x, "x")
-    px = _arg(x, torch.bfloat16, (T, H), dev, "x")
+    T, H, dev, px = _matrix(x, torch.bfloat16, "x")
     pw = _arg(weight, torch.bfloat16, (H,), dev, "weight")
     codes, pc = _out(codes, x, torch.int8, (T, H), dev, "codes")
     scales, ps = _out(scales, x, torch.float32, (T,), dev, "scales")
@@ -663,10 +672,10 @@ def moe_nvfp4_pre_norm_int8(x, weight, eps: float, codes=None, scales=None):
 def _gate(gate, T, H, dev):
     if gate is None:
         return None, 0, 0
-    rows, cols, _ = _rows(gate, "gate")
-    if rows not in (1, T) or cols not in (1, H):
-        raise ValueError(f"gate: expected a shape that broadcasts to {(T, H)}")
-    return _arg(gate, torch.bfloat16, (rows, cols), dev, "gate"), rows, cols
+    rows, cols, where, address = _matrix(gate, torch.bfloat16, "gate")
+    if rows not in (1, T) or cols not in (1, H) or where != dev:
+        raise ValueError(f"gate: expected a shape that broadcasts to {(T, H)}, on cuda:{dev}")
+    return address, rows, cols
 
 
 def moe_nvfp4_post_norm(y, weight, residual, eps: float, gate=None, residual_scale: float = 1.0,
@@ -674,9 +683,8 @@ def moe_nvfp4_post_norm(y, weight, residual, eps: float, gate=None, residual_sca
     """out = residual_scale * residual + gate * norm(y), with the norm of moe_nvfp4_pre_norm;
     gate bf16 [1 or T, 1 or H] or None.  With next_weight [H] also the following block's
     pre-norm of out.  Returns out bf16 [T, H], or (out, next)."""
-    T, H, dev = _rows(y, "y")
     bf = torch.bfloat16
-    py = _arg(y, bf, (T, H), dev, "y")
+    T, H, dev, py = _matrix(y, bf, "y")
     pw = _arg(weight, bf, (H,), dev, "weight")
     pr = _arg(residual, bf, (T, H), dev, "residual")
     pg, rows, cols = _gate(gate, T, H, dev)
@@ -700,10 +708,9 @@ def moe_nvfp4_pre_norm_backward(dy, x, weight, eps: float, dskip=None, dx=None, 
                                 workspace=None):
     """Gradients of moe_nvfp4_pre_norm; dskip [T, H] (the gradient that reaches x past the
     block) is added to dx.  Returns (dx bf16 [T, H], dweight bf16 [H])."""
-    T, H, dev = _rows(x, "x")
     bf = torch.bfloat16
+    T, H, dev, px = _matrix(x, bf, "x")
     pd = _arg(dy, bf, (T, H), dev, "dy")
-    px = _arg(x, bf, (T, H), dev, "x")
     pw = _arg(weight, bf, (H,), dev, "weight")
     ps = _optional(dskip, bf, (T, H), dev, "dskip")
     dx, pdx = _out(dx, x, bf, (T, H), dev, "dx")
@@ -726,10 +733,9 @@ def moe_nvfp4_post_norm_backward(dout, y, weight, eps: float, gate=None,
     """Gradients of moe_nvfp4_post_norm's out.  Returns (dy bf16 [T, H], dweight bf16 [H],
     dgate of gate's shape or None without a gate, dresidual bf16 [T, H] or None when
     need_dresidual is false)."""
-    T, H, dev = _rows(y, "y")
     bf = torch.bfloat16
+    T, H, dev, py = _matrix(y, bf, "y")
     pd = _arg(dout, bf, (T, H), dev, "dout")
-    py = _arg(y, bf, (T, H), dev, "y")
     pw = _arg(weight, bf, (H,), dev, "weight")
     pg, rows, cols = _gate(gate, T, H, dev)
     dy, pdy = _out(dy, y, bf, (T, H), dev, "dy")
@@ -747,16 +753,21 @@ def moe_nvfp4_post_norm_backward(dout, y, weight, eps: float, gate=None,
     return dy, dweight, dgate, dresidual
 
 
+def _gate_up_rows(w_gu, H, dev):
+    rows, address = _weight(w_gu, torch.bfloat16, H, dev, "w_gu")
+    if rows % 2:
+        raise ValueError("w_gu: expected gate rows and as many up rows")
+    return rows // 2, address
+
+
 def moe_nvfp4_gate_up(x, w_gu, act: int = ACT_SILU, h=None, gu=None,
                       error_flag=None) -> torch.Tensor:
     """h = act(x W_g^T) * (x W_u^T) in one kernel; x bf16 [T, H]; w_gu bf16 [2I, H], gate rows
     first.  gu bf16 [T, 2I], when given, receives the pre-activations that
     moe_nvfp4_gate_up_backward takes.  Returns h bf16 [T, I]."""
-    T, H, dev = _rows(x, "x")
     bf = torch.bfloat16
-    I = _rows(w_gu, "w_gu")[0] // 2
-    px = _arg(x, bf, (T, H), dev, "x")
-    pw = _arg(w_gu, bf, (2 * I, H), dev, "w_gu")
+    T, H, dev, px = _matrix(x, bf, "x")
+    I, pw = _gate_up_rows(w_gu, H, dev)
     h, ph = _out(h, x, bf, (T, I), dev, "h")
     pgu = _optional(gu, bf, (T, 2 * I), dev, "gu")
     _run("moe_nvfp4_gate_up", dev, px, pw, T, H, I, act, ph, pgu, _flag(error_flag, dev))
@@ -772,12 +783,10 @@ def moe_nvfp4_gate_up_backward(dh, x, w_gu, gu, act: int = ACT_SILU, dx=None, dw
                                error_flag=None):
     """Gradients of moe_nvfp4_gate_up from dh bf16 [T, I] and the kept gu.  Returns
     (dx bf16 [T, H], dw_gu bf16 [2I, H]), None in the place of one that is not needed."""
-    T, H, dev = _rows(x, "x")
     bf = torch.bfloat16
-    I = _rows(w_gu, "w_gu")[0] // 2
+    T, H, dev, px = _matrix(x, bf, "x")
+    I, pw = _gate_up_rows(w_gu, H, dev)
     pd = _arg(dh, bf, (T, I), dev, "dh")
-    px = _arg(x, bf, (T, H), dev, "x")
-    pw = _arg(w_gu, bf, (2 * I, H), dev, "w_gu")
     pgu = _arg(gu, bf, (T, 2 * I), dev, "gu")
     pdx = pdw = None
     if need_dx or dx is not None:
@@ -793,8 +802,7 @@ def moe_nvfp4_gate_up_backward(dh, x, w_gu, gu, act: int = ACT_SILU, dx=None, dw
 def nvfp4_int8_quantize(x, codes=None, scales=None):
     """Rows of x bf16 [rows, cols] -> (codes int8 [rows, cols], scales fp32 [rows]):
     scale = max |x| / 127, code = the integer nearest to x / scale."""
-    T, K, dev = _rows(x, "x")
-    px = _arg(x, torch.bfloat16, (T, K), dev, "x")
+    T, K, dev, px = _matrix(x, torch.bfloat16, "x")
     codes, pc = _out(codes, x, torch.int8, (T, K), dev, "codes")
     scales, ps = _out(scales, x, torch.float32, (T,), dev, "scales")
     _run("nvfp4_int8_quantize", dev, px, T, K, pc, ps)
@@ -804,10 +812,8 @@ def nvfp4_int8_quantize(x, codes=None, scales=None):
 def nvfp4_int8_matmul(a, a_scales, w, w_scales, out=None, error_flag=None) -> torch.Tensor:
     """bf16 [T, N] = (a [T, K] int8 times w [N, K] int8 transposed, exact) scaled by a_scales
     fp32 [T] and w_scales fp32 [N]."""
-    T, K, dev = _rows(a, "a")
-    N = _rows(w, "w")[0]
-    pa = _arg(a, torch.int8, (T, K), dev, "a")
-    pw = _arg(w, torch.int8, (N, K), dev, "w")
+    T, K, dev, pa = _matrix(a, torch.int8, "a")
+    N, pw = _weight(w, torch.int8, K, dev, "w")
     pas = _arg(a_scales, torch.float32, (T,), dev, "a_scales")
     pws = _arg(w_scales, torch.float32, (N,), dev, "w_scales")
     out, po = _out(out, a, torch.bfloat16, (T, N), dev, "out")

@@ -141,3 +141,35 @@ def test_a_block_between_its_norms(nv, T):
         assert err <= bound, (err, bound)
     deq = q.cpu().double() * s.cpu().double()[:, None]
     assert ((deq - n1d).abs() <= 0.51 * s.cpu().double()[:, None]).all()
+
+
+def test_binding_refuses_what_does_not_fit(nv):
+    """Shapes, types, strides and mixed devices, each with a ValueError; wrong numbers of rows
+    and the library's own limits with its status."""
+    a, sa, w, sw = (t.cuda() for t in case(3, 64, 64))
+    x, wt = torch.zeros(3, 64).bfloat16().cuda(), torch.ones(64).bfloat16().cuda()
+    wg = torch.zeros(32, 64).bfloat16().cuda()
+    bad = [lambda: nv.nvfp4_int8_matmul(a, sa, w[:, :32].contiguous(), sw),
+           lambda: nv.nvfp4_int8_matmul(a, sa, w.cpu(), sw),
+           lambda: nv.nvfp4_int8_matmul(a, sa[:2], w, sw),
+           lambda: nv.nvfp4_int8_matmul(a, sa, w, sw.double()),
+           lambda: nv.nvfp4_int8_matmul(a.t(), sa, w, sw),
+           lambda: nv.nvfp4_int8_matmul(a, sa, w, sw, out=torch.empty(3, 64).cuda()),
+           lambda: nv.nvfp4_int8_quantize(x[:, ::2]), lambda: nv.nvfp4_int8_quantize(x[0]),
+           lambda: nv.moe_nvfp4_pre_norm(x.float(), wt, EPS),
+           lambda: nv.moe_nvfp4_pre_norm(x, wt[:32], EPS),
+           lambda: nv.moe_nvfp4_post_norm(x, wt, x, EPS, gate=x[:2]),
+           lambda: nv.moe_nvfp4_post_norm(x, wt, x, EPS, next_out=x),
+           lambda: nv.moe_nvfp4_post_norm_backward(x, x, wt, EPS, dgate=x),
+           lambda: nv.moe_nvfp4_pre_norm_backward(x, x, wt, EPS, workspace=x),
+           lambda: nv.moe_nvfp4_gate_up(x, wg[:31]), lambda: nv.moe_nvfp4_gate_up(x, wg.t()),
+           lambda: nv.moe_nvfp4_gate_up_backward(x, x, wg, x)]
+    for call in bad:
+        with pytest.raises(ValueError):
+            call()
+    small = torch.empty(64, dtype=torch.uint8, device="cuda")
+    for call in (lambda: nv.moe_nvfp4_pre_norm_backward(x, x, wt, EPS, workspace=small),
+                 lambda: nv.moe_nvfp4_gate_up(x, wg, act=5), lambda: nv.moe_nvfp4_pre_norm(x, wt, 0.0),
+                 lambda: nv.moe_nvfp4_gate_up(x[:, :36].contiguous(), wg[:, :36].contiguous())):
+        with pytest.raises(nv.NVFP4Error):
+            call()
