@@ -173,3 +173,40 @@ def test_binding_refuses_what_does_not_fit(nv):
                  lambda: nv.moe_nvfp4_gate_up(x[:, :36].contiguous(), wg[:, :36].contiguous())):
         with pytest.raises(nv.NVFP4Error):
             call()
+
+
+def test_many_calls_on_several_streams(nv):
+    """Every operator, few and many tokens, again and again on three streams at once: each
+    result is bit for bit what the operator gives alone."""
+    H, I, N = 512, 768, 1032
+    g = torch.Generator().manual_seed(3)
+    r = lambda *s: torch.randn(s, generator=g).bfloat16().cuda()
+    w, w_gu, gate = r(H), r(2 * I, H) * 0.05, r(1, H)
+    wq = torch.randint(-127, 128, (N, H), generator=g, dtype=torch.int8).cuda()
+    ws = torch.rand(N, generator=g).cuda()
+
+    def step(x, dh):
+        T = x.shape[0]
+        y = nv.moe_nvfp4_pre_norm(x, w, EPS)
+        gu = torch.empty(T, 2 * I, dtype=torch.bfloat16, device="cuda")
+        h = nv.moe_nvfp4_gate_up(y, w_gu, gu=gu)
+        dx, dw = nv.moe_nvfp4_gate_up_backward(dh, y, w_gu, gu)
+        q = nv.nvfp4_int8_matmul(*nv.moe_nvfp4_pre_norm_int8(x, w, EPS), wq, ws)
+        o = nv.moe_nvfp4_post_norm(y, w, x, EPS, gate=gate, next_weight=w)
+        b = nv.moe_nvfp4_post_norm_backward(dx, y, w, EPS, gate=gate)
+        return (y, gu, h, dx, dw, q) + o + b
+
+    sizes = (1, 40, 1500)
+    data = [(r(T, H), r(T, I)) for T in sizes]
+    want = [step(*d) for d in data]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sizes]
+    for _ in range(5):
+        got = []
+        for k in range(4):
+            for s, d in zip(streams, data[k % 3:] + data[:k % 3]):
+                with torch.cuda.stream(s):
+                    got.append((len(d[0]), step(*d)))
+        torch.cuda.synchronize()
+        for T, o in got:
+            assert all(torch.equal(p, q) for p, q in zip(o, want[sizes.index(T)]))
