@@ -13,6 +13,7 @@ Format (page "GLM-5-NVFP4-MTP", "Model Description"): 4-bit E2M1 values, one E4M
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -720,6 +721,7 @@ def moe_nvfp4_pre_norm_backward(dy, x, weight, eps: float, dskip=None, dx=None, 
     return dx, dweight
 
 
+@functools.lru_cache(maxsize=256)   # a size: it depends on the arguments alone
 def _norm_scratch(T, H, dev):
     if dev == _current_device():
         return _lib().moe_nvfp4_norm_backward_workspace_size(T, H)
