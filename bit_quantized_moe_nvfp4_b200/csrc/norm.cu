@@ -154,8 +154,8 @@ __device__ __forceinline__ uint2 codes8(const float2 (&y)[4], float inv) {
   }
   return make_uint2(low_bytes(q[0], q[1], q[2], q[3]), low_bytes(q[4], q[5], q[6], q[7]));
 }
-// Power of two that brings a row of this amax to where 127 / amax and its split neither
-// overflow nor underflow, and the scale of the row.
+// Power of two that brings a row of this amax to where 127 / amax neither overflows nor
+// underflows, that quotient, and the scale of the row.
 __device__ __forceinline__ float code_range(float amax) {
   return amax > 0x1p60f ? 0x1p-64f : amax < 0x1p-60f ? 0x1p+76f : 1.f;
 }
@@ -444,6 +444,8 @@ __global__ void __launch_bounds__(max_threads<MAXT>(), grad_row_ctas(MAXT, VPT, 
   for (int64_t t = t0; t < p.T; t += step) {
     cp_async_wait(rows.stages - 1);
     const uint32_t at = feed.stage_at(stage);
+    // read before the reduction: its gradient may be written over it after
+    const float g1 = GATE == kRowGate ? __bfloat162float(p.gate[t * p.gt]) : 1.f;
     // sums of x^2, and of d w x (times the gate where it has a value for each channel)
     float2 sx = both(0.f), sd = both(0.f);
 #pragma unroll
@@ -469,7 +471,6 @@ __global__ void __launch_bounds__(max_threads<MAXT>(), grad_row_ctas(MAXT, VPT, 
     float s[2] = {sx.x + sx.y, sd.x + sd.y};
     reduce_row<WARP, Sum>(s, buf, turn);
     const float r = rsqrtf(fmaf(s[0], inv_h, p.eps));
-    const float g1 = GATE == kRowGate ? __bfloat162float(p.gate[t * p.gt]) : 1.f;
     const float rg = r * g1;
     const float k = rg * r * (r * s[1] * inv_h);   // r mean(dn n) r: dx = r dn - k x
     if (GATE == kRowGate) {

@@ -235,6 +235,10 @@ def test_in_place(nv, T, H):
     got = nv.moe_nvfp4_post_norm_backward(a, b, w, EPS, gate=c, residual_scale=0.5, dy=b,
                                           dgate=c, dresidual=a)
     assert all(torch.equal(p, q) for p, q in zip(got, want))
+    g1 = g[:, :1].contiguous()
+    want = nv.moe_nvfp4_post_norm_backward(d, y, w, EPS, gate=g1)
+    got = nv.moe_nvfp4_post_norm_backward(d, y, w, EPS, gate=g1, dgate=g1)
+    assert all(torch.equal(p, q) for p, q in zip(got, want))
 
 
 def test_rows_do_not_touch_each_other(nv):
