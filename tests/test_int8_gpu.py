@@ -210,3 +210,38 @@ def test_many_calls_on_several_streams(nv):
         torch.cuda.synchronize()
         for T, o in got:
             assert all(torch.equal(p, q) for p, q in zip(o, want[sizes.index(T)]))
+
+
+def test_weights_written_by_the_kernel_before(nv):
+    """Weights that the launch directly before writes, over and over into the same memory: the
+    product takes the new ones (it asks its first weights into L2 before that launch ends)."""
+    N, K, n = 4096, 1024, 12
+    g = torch.Generator().manual_seed(1)
+    ws_in = [torch.randn(N, K, generator=g).bfloat16().cuda() for _ in range(n)]
+    a, sa, _, _ = (t.cuda() for t in case(3, 8, K))
+    want = []
+    for w in ws_in:
+        wq, ws = nv.nvfp4_int8_quantize(w)
+        torch.cuda.synchronize()
+        want.append(nv.nvfp4_int8_matmul(a, sa, wq, ws))
+    wq = torch.empty(N, K, dtype=torch.int8, device="cuda")
+    ws = torch.empty(N, device="cuda")
+    outs = [torch.empty(3, N, dtype=torch.bfloat16, device="cuda") for _ in range(n)]
+
+    def chain():
+        for w, o in zip(ws_in, outs):
+            nv.nvfp4_int8_quantize(w, codes=wq, scales=ws)
+            nv.nvfp4_int8_matmul(a, sa, wq, ws, out=o)
+
+    chain()
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, w) for o, w in zip(outs, want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        chain()
+    for _ in range(20):
+        for o in outs:
+            o.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, w) for o, w in zip(outs, want))
