@@ -594,13 +594,18 @@ def _optional(t, dtype, shape, dev: int, name: str):
 
 def _out(t, like, dtype, shape, dev: int, name: str):
     """(`t`, or a new tensor beside `like`; its address)."""
-    if t is not None:
-        return t, _arg(t, dtype, shape, dev, name)
-    if like.shape != shape:
+    if t is None:
         t = torch.empty(*shape, dtype=dtype, device=like.device)
-    else:   # empty_like is the quicker of the two, and quicker still without a dtype
-        t = torch.empty_like(like) if like.dtype is dtype else torch.empty_like(like, dtype=dtype)
-    return t, t.data_ptr()
+        return t, t.data_ptr()
+    return t, _arg(t, dtype, shape, dev, name)
+
+
+def _twin(t, like, dev: int, name: str):
+    """_out with the type and shape of `like` (empty_like is quicker than empty)."""
+    if t is None:
+        t = torch.empty_like(like)
+        return t, t.data_ptr()
+    return t, _arg(t, like.dtype, like.shape, dev, name)
 
 
 def _matrix(x, dtype, name: str):
@@ -634,14 +639,13 @@ def _scratch(workspace, nbytes: int, like):
     return workspace, workspace.data_ptr(), workspace.numel()
 
 
-def _run(name: str, dev: int, *args) -> None:
-    """Call an entry point on CUDA device `dev` and that device's current stream."""
-    f = getattr(_LIB or _lib(), name)
-    if dev == _current_device():
-        status = f(*args, _raw_stream(dev))
-    else:
-        with torch.cuda.device(dev):
-            status = f(*args, _raw_stream(dev))
+def _on(dev: int, call, *args):
+    """call(*args) with CUDA device `dev` current."""
+    with torch.cuda.device(dev):
+        return call(*args)
+
+
+def _done(status: int) -> None:
     if status:
         _check(status)
 
@@ -653,9 +657,11 @@ def _flag(error_flag, dev: int):
 def moe_nvfp4_pre_norm(x, weight, eps: float, out=None) -> torch.Tensor:
     """weight * x / sqrt(mean(x^2) + eps) for each row of x bf16 [T, H]; weight bf16 [H]."""
     T, H, dev, px = _matrix(x, torch.bfloat16, "x")
+    if dev != _current_device():
+        return _on(dev, moe_nvfp4_pre_norm, x, weight, eps, out)
     pw = _arg(weight, torch.bfloat16, (H,), dev, "weight")
-    out, po = _out(out, x, torch.bfloat16, (T, H), dev, "out")
-    _run("moe_nvfp4_pre_norm", dev, px, pw, T, H, eps, po)
+    out, po = _twin(out, x, dev, "out")
+    _done((_LIB or _lib()).moe_nvfp4_pre_norm(px, pw, T, H, eps, po, _raw_stream(dev)))
     return out
 
 
@@ -663,10 +669,12 @@ def moe_nvfp4_pre_norm_int8(x, weight, eps: float, codes=None, scales=None):
     """moe_nvfp4_pre_norm's rows as 8-bit codes and one scale each, for nvfp4_int8_matmul.
     Returns (codes int8 [T, H], scales fp32 [T])."""
     T, H, dev, px = _matrix(x, torch.bfloat16, "x")
+    if dev != _current_device():
+        return _on(dev, moe_nvfp4_pre_norm_int8, x, weight, eps, codes, scales)
     pw = _arg(weight, torch.bfloat16, (H,), dev, "weight")
     codes, pc = _out(codes, x, torch.int8, (T, H), dev, "codes")
     scales, ps = _out(scales, x, torch.float32, (T,), dev, "scales")
-    _run("moe_nvfp4_pre_norm_int8", dev, px, pw, T, H, eps, pc, ps)
+    _done((_LIB or _lib()).moe_nvfp4_pre_norm_int8(px, pw, T, H, eps, pc, ps, _raw_stream(dev)))
     return codes, scales
 
 
@@ -686,18 +694,21 @@ def moe_nvfp4_post_norm(y, weight, residual, eps: float, gate=None, residual_sca
     pre-norm of out.  Returns out bf16 [T, H], or (out, next)."""
     bf = torch.bfloat16
     T, H, dev, py = _matrix(y, bf, "y")
+    if dev != _current_device():
+        return _on(dev, moe_nvfp4_post_norm, y, weight, residual, eps, gate, residual_scale,
+                   next_weight, out, next_out)
     pw = _arg(weight, bf, (H,), dev, "weight")
     pr = _arg(residual, bf, (T, H), dev, "residual")
     pg, rows, cols = _gate(gate, T, H, dev)
     pn = _optional(next_weight, bf, (H,), dev, "next_weight")
     if pn is None and next_out is not None:
         raise ValueError("next_out needs next_weight")
-    out, po = _out(out, y, bf, (T, H), dev, "out")
+    out, po = _twin(out, y, dev, "out")
     po2 = None
     if pn is not None:
-        next_out, po2 = _out(next_out, y, bf, (T, H), dev, "next_out")
-    _run("moe_nvfp4_post_norm", dev, py, pw, pr, pg, T, H, rows, cols, eps, residual_scale, pn,
-         po, po2)
+        next_out, po2 = _twin(next_out, y, dev, "next_out")
+    _done((_LIB or _lib()).moe_nvfp4_post_norm(
+        py, pw, pr, pg, T, H, rows, cols, eps, residual_scale, pn, po, po2, _raw_stream(dev)))
     return out if pn is None else (out, next_out)
 
 
@@ -711,22 +722,23 @@ def moe_nvfp4_pre_norm_backward(dy, x, weight, eps: float, dskip=None, dx=None, 
     block) is added to dx.  Returns (dx bf16 [T, H], dweight bf16 [H])."""
     bf = torch.bfloat16
     T, H, dev, px = _matrix(x, bf, "x")
+    if dev != _current_device():
+        return _on(dev, moe_nvfp4_pre_norm_backward, dy, x, weight, eps, dskip, dx, dweight,
+                   workspace)
     pd = _arg(dy, bf, (T, H), dev, "dy")
     pw = _arg(weight, bf, (H,), dev, "weight")
     ps = _optional(dskip, bf, (T, H), dev, "dskip")
-    dx, pdx = _out(dx, x, bf, (T, H), dev, "dx")
-    dweight, pdw = _out(dweight, weight, bf, (H,), dev, "dweight")
+    dx, pdx = _twin(dx, x, dev, "dx")
+    dweight, pdw = _twin(dweight, weight, dev, "dweight")
     workspace, pws, nws = _scratch(workspace, _norm_scratch(T, H, dev), x)
-    _run("moe_nvfp4_pre_norm_backward", dev, pd, px, pw, ps, T, H, eps, pdx, pdw, pws, nws)
+    _done((_LIB or _lib()).moe_nvfp4_pre_norm_backward(
+        pd, px, pw, ps, T, H, eps, pdx, pdw, pws, nws, _raw_stream(dev)))
     return dx, dweight
 
 
 @functools.lru_cache(maxsize=256)   # a size: it depends on the arguments alone
 def _norm_scratch(T, H, dev):
-    if dev == _current_device():
-        return _lib().moe_nvfp4_norm_backward_workspace_size(T, H)
-    with torch.cuda.device(dev):
-        return _lib().moe_nvfp4_norm_backward_workspace_size(T, H)
+    return _lib().moe_nvfp4_norm_backward_workspace_size(T, H)   # of the current device, dev
 
 
 def moe_nvfp4_post_norm_backward(dout, y, weight, eps: float, gate=None,
@@ -737,21 +749,25 @@ def moe_nvfp4_post_norm_backward(dout, y, weight, eps: float, gate=None,
     need_dresidual is false)."""
     bf = torch.bfloat16
     T, H, dev, py = _matrix(y, bf, "y")
+    if dev != _current_device():
+        return _on(dev, moe_nvfp4_post_norm_backward, dout, y, weight, eps, gate, residual_scale,
+                   dy, dweight, dgate, dresidual, need_dresidual, workspace)
     pd = _arg(dout, bf, (T, H), dev, "dout")
     pw = _arg(weight, bf, (H,), dev, "weight")
     pg, rows, cols = _gate(gate, T, H, dev)
-    dy, pdy = _out(dy, y, bf, (T, H), dev, "dy")
-    dweight, pdw = _out(dweight, weight, bf, (H,), dev, "dweight")
+    dy, pdy = _twin(dy, y, dev, "dy")
+    dweight, pdw = _twin(dweight, weight, dev, "dweight")
     pdg = pdr = None
     if gate is not None:
-        dgate, pdg = _out(dgate, gate, bf, (rows, cols), dev, "dgate")
+        dgate, pdg = _twin(dgate, gate, dev, "dgate")
     elif dgate is not None:
         raise ValueError("dgate needs gate")
     if need_dresidual or dresidual is not None:
-        dresidual, pdr = _out(dresidual, y, bf, (T, H), dev, "dresidual")
+        dresidual, pdr = _twin(dresidual, y, dev, "dresidual")
     workspace, pws, nws = _scratch(workspace, _norm_scratch(T, H, dev), y)
-    _run("moe_nvfp4_post_norm_backward", dev, pd, py, pw, pg, T, H, rows, cols, eps,
-         residual_scale, pdy, pdw, pdg, pdr, pws, nws)
+    _done((_LIB or _lib()).moe_nvfp4_post_norm_backward(
+        pd, py, pw, pg, T, H, rows, cols, eps, residual_scale, pdy, pdw, pdg, pdr, pws, nws,
+        _raw_stream(dev)))
     return dy, dweight, dgate, dresidual
 
 
@@ -769,10 +785,13 @@ def moe_nvfp4_gate_up(x, w_gu, act: int = ACT_SILU, h=None, gu=None,
     moe_nvfp4_gate_up_backward takes.  Returns h bf16 [T, I]."""
     bf = torch.bfloat16
     T, H, dev, px = _matrix(x, bf, "x")
+    if dev != _current_device():
+        return _on(dev, moe_nvfp4_gate_up, x, w_gu, act, h, gu, error_flag)
     I, pw = _gate_up_rows(w_gu, H, dev)
     h, ph = _out(h, x, bf, (T, I), dev, "h")
     pgu = _optional(gu, bf, (T, 2 * I), dev, "gu")
-    _run("moe_nvfp4_gate_up", dev, px, pw, T, H, I, act, ph, pgu, _flag(error_flag, dev))
+    _done((_LIB or _lib()).moe_nvfp4_gate_up(
+        px, pw, T, H, I, act, ph, pgu, _flag(error_flag, dev), _raw_stream(dev)))
     return h
 
 
@@ -787,17 +806,21 @@ def moe_nvfp4_gate_up_backward(dh, x, w_gu, gu, act: int = ACT_SILU, dx=None, dw
     (dx bf16 [T, H], dw_gu bf16 [2I, H]), None in the place of one that is not needed."""
     bf = torch.bfloat16
     T, H, dev, px = _matrix(x, bf, "x")
+    if dev != _current_device():
+        return _on(dev, moe_nvfp4_gate_up_backward, dh, x, w_gu, gu, act, dx, dw_gu, need_dx,
+                   need_dw, workspace, error_flag)
     I, pw = _gate_up_rows(w_gu, H, dev)
     pd = _arg(dh, bf, (T, I), dev, "dh")
     pgu = _arg(gu, bf, (T, 2 * I), dev, "gu")
     pdx = pdw = None
     if need_dx or dx is not None:
-        dx, pdx = _out(dx, x, bf, (T, H), dev, "dx")
+        dx, pdx = _twin(dx, x, dev, "dx")
     if need_dw or dw_gu is not None:
-        dw_gu, pdw = _out(dw_gu, w_gu, bf, (2 * I, H), dev, "dw_gu")
+        dw_gu, pdw = _twin(dw_gu, w_gu, dev, "dw_gu")
     workspace, pws, nws = _scratch(workspace, moe_nvfp4_gate_up_backward_workspace_size(T, I), x)
-    _run("moe_nvfp4_gate_up_backward", dev, pd, px, pw, pgu, T, H, I, act, pdx, pdw, pws, nws,
-         _flag(error_flag, dev))
+    _done((_LIB or _lib()).moe_nvfp4_gate_up_backward(
+        pd, px, pw, pgu, T, H, I, act, pdx, pdw, pws, nws, _flag(error_flag, dev),
+        _raw_stream(dev)))
     return dx, dw_gu
 
 
@@ -805,9 +828,11 @@ def nvfp4_int8_quantize(x, codes=None, scales=None):
     """Rows of x bf16 [rows, cols] -> (codes int8 [rows, cols], scales fp32 [rows]):
     scale = max |x| / 127, code = the integer nearest to x / scale."""
     T, K, dev, px = _matrix(x, torch.bfloat16, "x")
+    if dev != _current_device():
+        return _on(dev, nvfp4_int8_quantize, x, codes, scales)
     codes, pc = _out(codes, x, torch.int8, (T, K), dev, "codes")
     scales, ps = _out(scales, x, torch.float32, (T,), dev, "scales")
-    _run("nvfp4_int8_quantize", dev, px, T, K, pc, ps)
+    _done((_LIB or _lib()).nvfp4_int8_quantize(px, T, K, pc, ps, _raw_stream(dev)))
     return codes, scales
 
 
@@ -815,11 +840,14 @@ def nvfp4_int8_matmul(a, a_scales, w, w_scales, out=None, error_flag=None) -> to
     """bf16 [T, N] = (a [T, K] int8 times w [N, K] int8 transposed, exact) scaled by a_scales
     fp32 [T] and w_scales fp32 [N]."""
     T, K, dev, pa = _matrix(a, torch.int8, "a")
+    if dev != _current_device():
+        return _on(dev, nvfp4_int8_matmul, a, a_scales, w, w_scales, out, error_flag)
     N, pw = _weight(w, torch.int8, K, dev, "w")
     pas = _arg(a_scales, torch.float32, (T,), dev, "a_scales")
     pws = _arg(w_scales, torch.float32, (N,), dev, "w_scales")
     out, po = _out(out, a, torch.bfloat16, (T, N), dev, "out")
-    _run("nvfp4_int8_matmul", dev, pa, pas, pw, pws, T, N, K, po, _flag(error_flag, dev))
+    _done((_LIB or _lib()).nvfp4_int8_matmul(
+        pa, pas, pw, pws, T, N, K, po, _flag(error_flag, dev), _raw_stream(dev)))
     return out
 
 

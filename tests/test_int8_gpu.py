@@ -245,3 +245,29 @@ def test_weights_written_by_the_kernel_before(nv):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(o, w) for o, w in zip(outs, want))
+
+
+def test_calls_from_another_current_device(nv, monkeypatch):
+    """A call on tensors of a device that is not the current one is made again with it current
+    and gives the same (the other device is feigned: the first look answers 1)."""
+    a, sa, w, sw = (t.cuda() for t in case(5, 64, 64))
+    g = torch.Generator().manual_seed(2)
+    r = lambda *s: torch.randn(s, generator=g).bfloat16().cuda()
+    x, d, wt, gate, wg, dh, gu = r(5, 64), r(5, 64), r(64), r(1, 64), r(32, 64), r(5, 16), r(5, 32)
+    calls = [lambda: nv.nvfp4_int8_quantize(x), lambda: nv.nvfp4_int8_matmul(a, sa, w, sw),
+             lambda: nv.moe_nvfp4_pre_norm(x, wt, EPS), lambda: nv.moe_nvfp4_pre_norm_int8(x, wt, EPS),
+             lambda: nv.moe_nvfp4_pre_norm_backward(d, x, wt, EPS, dskip=d),
+             lambda: nv.moe_nvfp4_post_norm(x, wt, d, EPS, gate=gate, residual_scale=0.5,
+                                            next_weight=wt),
+             lambda: nv.moe_nvfp4_post_norm_backward(d, x, wt, EPS, gate=gate, residual_scale=0.5),
+             lambda: nv.moe_nvfp4_gate_up(x, wg, act=nv.ACT_GELU),
+             lambda: nv.moe_nvfp4_gate_up_backward(dh, x, wg, gu, act=nv.ACT_GELU)]
+    for call in calls:
+        want = call()
+        looks = iter([1, 0])
+        with monkeypatch.context() as m:
+            m.setattr(nv, "_current_device", lambda: next(looks))
+            got = call()
+        assert next(looks, None) is None   # looked twice: refused, then taken
+        for p, q in zip(*(t if isinstance(t, tuple) else (t,) for t in (got, want))):
+            assert torch.equal(p, q)
