@@ -631,7 +631,7 @@ def _weight(w, dtype, cols: int, dev: int, name: str):
 def _scratch(workspace, nbytes: int, like):
     """(workspace, its address, its bytes), allocated beside `like` when none is given."""
     if workspace is None:
-        workspace = like.new_empty((nbytes,), dtype=torch.uint8)
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
     elif workspace.dtype is not torch.uint8 or workspace.get_device() != like.get_device() \
             or not workspace.is_contiguous():
         raise ValueError("workspace: expected a contiguous torch.uint8 tensor on the inputs' "
