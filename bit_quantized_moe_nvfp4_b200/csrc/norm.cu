@@ -131,26 +131,30 @@ __device__ __forceinline__ void clear_reduce(float (&buf)[N]) {
 }
 
 // Codes of 8 values: the integers nearest to 127 y / amax, ties to even, without a division
-// for each.  With inv = fl(127 / amax), v = fl(y inv) is off by at most 2^-23 relative.  A
-// quotient of 127 p / q with p, q < 2^8 (bf16 significands) and a power of two is either a tie
-// (k + 1/2, at most 9 bits) or at least 2^-16 relative away from one.  So v rounded to 18
-// significant bits (in its bit pattern) is the tie itself where there is one and stays on its
-// side otherwise, and rounding that to an integer rounds as the real quotient does.  Adding
-// 1.5 2^23 rounds to the integer, whose low byte is then the code.
+// for each.  With inv = fl(127 / amax), v = fl(y inv) is off by at most 2^-23 relative; adding
+// 1.5 2^23 rounds it to the integer, whose low byte is then the code.
+// BF16: where y and amax are bf16 values, a quotient of 127 p / q with p, q < 2^8 (their
+// significands) and a power of two is either a tie (k + 1/2, at most 9 bits) or at least 2^-16
+// relative away from one.  So v rounded to 18 significant bits (in its bit pattern) first is the
+// tie itself where there is one and stays on its side otherwise, and the code is the real
+// quotient's.  Other values can lie next to a tie, where that step would move them onto it: they
+// are rounded once, as they are.
+template <bool BF16>
 __device__ __forceinline__ uint32_t code_bits(float v) {
-  const uint32_t hi = (__float_as_uint(v) + 32u) & ~63u;
-  return __float_as_uint(__uint_as_float(hi) + 12582912.f);
+  if (BF16) v = __uint_as_float((__float_as_uint(v) + 32u) & ~63u);
+  return __float_as_uint(v + 12582912.f);
 }
 __device__ __forceinline__ uint32_t low_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
 }
+template <bool BF16>
 __device__ __forceinline__ uint2 codes8(const float2 (&y)[4], float inv) {
   uint32_t q[8];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const float2 v = mul2(y[j], both(inv));
-    q[2 * j] = code_bits(v.x);
-    q[2 * j + 1] = code_bits(v.y);
+    q[2 * j] = code_bits<BF16>(v.x);
+    q[2 * j + 1] = code_bits<BF16>(v.y);
   }
   return make_uint2(low_bytes(q[0], q[1], q[2], q[3]), low_bytes(q[4], q[5], q[6], q[7]));
 }
@@ -342,7 +346,7 @@ __global__ void __launch_bounds__(max_threads<MAXT>(), row_ctas(MAXT))
         if (pre != 1.f)
 #pragma unroll
           for (int j = 0; j < 4; ++j) y[k][j] = mul2(y[k][j], both(pre));
-        out[me + i * tpr] = codes8(y[k], inv);
+        out[me + i * tpr] = codes8<MODE == kQuant>(y[k], inv);
       }
       if (me == 0) p.scales[t] = code_scale(am[0]);
     } else {

@@ -408,8 +408,9 @@ NVFP4_API int moe_nvfp4_forward_w4a4_profiled(
  * Errors: EINVAL, ESHAPE, EWORKSPACE (backward), ECUDA.
  *
  * moe_nvfp4_pre_norm, before a block:          out = weight n(x)
- * moe_nvfp4_pre_norm_int8, the same handed out as 8-bit rows for nvfp4_int8_matmul: codes
- * and scales are what nvfp4_int8_quantize gives for the unrounded weight n(x). */
+ * moe_nvfp4_pre_norm_int8, the same handed out as 8-bit rows for nvfp4_int8_matmul: codes and
+ * scales by nvfp4_int8_quantize's formulas from the unrounded weight n(x), the quotient
+ * 127 weight n(x) / amax in fp32 (7 2^-24 relative), rounded once. */
 NVFP4_API int moe_nvfp4_pre_norm(const __nv_bfloat16 *x, const __nv_bfloat16 *weight, int64_t T,
                                  int64_t H, float eps, __nv_bfloat16 *out, cudaStream_t stream);
 NVFP4_API int moe_nvfp4_pre_norm_int8(const __nv_bfloat16 *x, const __nv_bfloat16 *weight,

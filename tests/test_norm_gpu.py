@@ -312,3 +312,16 @@ def test_another_stream_and_a_graph(nv):
     torch.cuda.synchronize()
     assert torch.equal(a[0], want[0]) and torch.equal(a[1], want[1])
     assert torch.equal(b[0], dwant[0]) and torch.equal(b[1], dwant[1])
+
+
+@pytest.mark.parametrize("T,H", [(600, 6144), (3000, 1024), (40, 16384)])
+def test_pre_norm_int8_codes_are_the_nearest(nv, T, H):
+    """A code is the integer nearest to the fp32 quotient.  The row's r is a factor of both y
+    and amax and cancels; x r, times w, 127 / amax and the quotient are rounded once each (y and
+    amax each carry two of them): the quotient is off by at most 6 u of 127, 7 u with amax taken
+    from a neighbour of the largest value."""
+    x, w = draw(T + H, T, H), draw(H, H, std=0.1, mean=1.0)
+    codes, _ = nv.moe_nvfp4_pre_norm_int8(x.cuda(), w.cuda(), EPS)
+    y = w.double() * x.double()
+    q = 127 * y / y.abs().amax(-1, keepdim=True)
+    assert ((codes.cpu().double() - q).abs() <= 0.5 + 127 * 7 * U).all()
