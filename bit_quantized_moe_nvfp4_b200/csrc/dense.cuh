@@ -32,15 +32,16 @@ namespace nvfp4 {
 enum DenseKind { kBf16 = 0, kS8 = 1 };
 enum DenseEpi { kEpiStore = 0, kEpiScale = 1, kEpiGate = 2 };
 
-// act(z) and its slope: SiLU, or GELU by its tanh form.
-__device__ __forceinline__ float tanh_f32(float v) {
-  const float e = expf(-2.f * fabsf(v));
-  return copysignf((1.f - e) / (1.f + e), v);
-}
+// act(z): SiLU, or GELU by its tanh form, in which (1 + tanh v) / 2 = 1 / (1 + exp(-2 v)): one
+// quotient, as exact for negative z as for positive (1 + tanh v cancels there: 0.6% off at
+// z = -4.25, 35% at -5).
+constexpr float kGeluA = 0.7978845608028654f;    // v = A (z + B z^3), A = sqrt(2 / pi)
+constexpr float kGeluB = 0.044715f;
+__device__ __forceinline__ float gelu_v(float z) { return kGeluA * fmaf(kGeluB * z * z, z, z); }
 template <int ACT>
 __device__ __forceinline__ float gate_act(float z) {
   if (ACT == NVFP4_ACT_SILU) return silu_f32(z);
-  return 0.5f * z * (1.f + tanh_f32(0.7978845608028654f * fmaf(0.044715f * z * z, z, z)));
+  return z / (1.f + expf(-2.f * gelu_v(z)));
 }
 
 struct DenseArgs {

@@ -13,7 +13,8 @@ namespace {
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 
-// act(z) and act'(z)
+// act(z) and act'(z).  GELU: with s = 1 / (1 + exp(-2 v)), act = z s and its slope is
+// s (1 + 2 z (1 - s) v'); the smaller of s and 1 - s is the quotient e / (1 + e), not a difference.
 template <int ACT>
 __device__ __forceinline__ void act_grad(float z, float &a, float &da) {
   if (ACT == NVFP4_ACT_SILU) {
@@ -21,10 +22,12 @@ __device__ __forceinline__ void act_grad(float z, float &a, float &da) {
     a = z * s;
     da = s * fmaf(z, 1.f - s, 1.f);
   } else {
-    const float c = 0.7978845608028654f, z2 = z * z;
-    const float t = tanh_f32(c * fmaf(0.044715f * z2, z, z));
-    a = 0.5f * z * (1.f + t);
-    da = 0.5f * (1.f + t) + 0.5f * z * (1.f - t * t) * c * fmaf(3.f * 0.044715f, z2, 1.f);
+    const float v = gelu_v(z), e = expf(-2.f * fabsf(v));
+    const float big = 1.f / (1.f + e), small = e * big;
+    const float s = z < 0.f ? small : big, rest = z < 0.f ? big : small;
+    const float dv = kGeluA * fmaf(3.f * kGeluB, z * z, 1.f);
+    a = z * s;
+    da = s * fmaf(2.f * z * rest, dv, 1.f);
   }
 }
 

@@ -235,3 +235,40 @@ def test_another_stream_and_a_graph(nv):
         torch.cuda.synchronize()
         for got in (a, b, c):
             assert all(torch.equal(p, q) for p, q in zip(got, want))
+
+
+def gate_of(z, T, I, H=8):
+    """x, w_gu, gu, dh with which every row's pre-activations are z (I of them) and 1."""
+    x = torch.zeros(T, H, dtype=torch.bfloat16)
+    x[:, 0] = 1
+    w = torch.zeros(2 * I, H, dtype=torch.bfloat16)
+    w[:I, 0], w[I:, 0] = z, 1
+    gu = torch.cat([z, torch.ones(I).bfloat16()]).repeat(T, 1)
+    return x.cuda(), w.cuda(), gu.cuda(), torch.ones(T, I, dtype=torch.bfloat16).cuda()
+
+
+def gelu_64(z):
+    """GELU's tanh form without its cancellation: (1 + tanh v) / 2 = 1 / (1 + exp(-2 v))."""
+    return z * torch.sigmoid(2 * (2 / torch.pi) ** 0.5 * (z + 0.044715 * z ** 3))
+
+
+@pytest.mark.parametrize("T,I", [(1, 520), (40, 520), (700, 1032)])
+def test_gelu_of_negative_gates(nv, T, I):
+    """Where (1 + tanh v) / 2 is small, act and slope are as exact as elsewhere.  v is off by
+    5 u (u = 2^-24; constant, square, fma and product, the constant's own rounding), so exp(-2 v)
+    by 10 |v| u + 4 u, at |v| <= 43 (z >= -10) 434 u < 2^-15; sum, division and product add 4 u.
+    The slope's second factor 1 + 2 z (1 - s) v' is at least 1 in magnitude for z <= -2 and its
+    terms at most 2 (1 + |it|): below 20 u.  All within 2^-14, and the rounding to bf16."""
+    z = -torch.linspace(2, 10, I).bfloat16()
+    x, w, gu, dh = gate_of(z, T, I)
+    zd = z.double().requires_grad_()
+    ref = gelu_64(zd)
+    slope, = torch.autograd.grad(ref.sum(), zd)
+    h = nv.moe_nvfp4_gate_up(x, w, act=nv.ACT_GELU).cpu().double()
+    assert ((h - ref.detach()).abs() <= (B + 2.0 ** -14) * ref.detach().abs()).all()
+    # one row reaches dw (its column 0 is the sum of dg over the rows): dg itself
+    one = torch.zeros_like(x)
+    one[T - 1] = x[T - 1]
+    _, dw = nv.moe_nvfp4_gate_up_backward(dh, one, w, gu, act=nv.ACT_GELU)
+    got = dw[:I, 0].cpu().double()
+    assert ((got - slope).abs() <= (B + 2.0 ** -14) * slope.abs()).all()
