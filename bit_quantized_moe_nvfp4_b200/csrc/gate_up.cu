@@ -15,6 +15,8 @@ size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 
 // act(z) and act'(z).  GELU: with s = 1 / (1 + exp(-2 v)), act = z s and its slope is
 // s (1 + 2 z (1 - s) v'); the smaller of s and 1 - s is the quotient e / (1 + e), not a difference.
+// From |z| = 11 on it is 0 in fp32 and so is its product; there z is held at 32, lest z v'
+// overflow beside it.
 template <int ACT>
 __device__ __forceinline__ void act_grad(float z, float &a, float &da) {
   if (ACT == NVFP4_ACT_SILU) {
@@ -25,9 +27,10 @@ __device__ __forceinline__ void act_grad(float z, float &a, float &da) {
     const float v = gelu_v(z), e = expf(-2.f * fabsf(v));
     const float big = 1.f / (1.f + e), small = e * big;
     const float s = z < 0.f ? small : big, rest = z < 0.f ? big : small;
-    const float dv = kGeluA * fmaf(3.f * kGeluB, z * z, 1.f);
+    const float zc = fminf(fmaxf(z, -32.f), 32.f);
+    const float dv = kGeluA * fmaf(3.f * kGeluB, zc * zc, 1.f);
     a = z * s;
-    da = s * fmaf(2.f * z * rest, dv, 1.f);
+    da = s * fmaf(2.f * zc * rest, dv, 1.f);
   }
 }
 
@@ -57,7 +60,8 @@ __global__ void __launch_bounds__(256) gate_grad_kernel(const __nv_bfloat16 *gu,
       act_grad<ACT>(bf16_lo(g[k]), a0, s0);
       act_grad<ACT>(bf16_hi(g[k]), a1, s1);
       const float d0 = bf16_lo(d[k]), d1 = bf16_hi(d[k]);
-      og[k] = pack_bf16x2(d0 * bf16_lo(u[k]) * s0, d1 * bf16_hi(u[k]) * s1);
+      // the slope first: it is at most 1.13, so nothing overflows that the result does not
+      og[k] = pack_bf16x2(d0 * (bf16_lo(u[k]) * s0), d1 * (bf16_hi(u[k]) * s1));
       ou[k] = pack_bf16x2(d0 * a0, d1 * a1);
     }
     uint4 *o = reinterpret_cast<uint4 *>(dgu + t * 2 * I);

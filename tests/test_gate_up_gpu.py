@@ -272,3 +272,59 @@ def test_gelu_of_negative_gates(nv, T, I):
     _, dw = nv.moe_nvfp4_gate_up_backward(dh, one, w, gu, act=nv.ACT_GELU)
     got = dw[:I, 0].cpu().double()
     assert ((got - slope).abs() <= (B + 2.0 ** -14) * slope.abs()).all()
+
+
+@pytest.mark.parametrize("T,I", [(1, 8), (700, 1032)])
+def test_huge_gates(nv, T, I):
+    """Gates whose square or cube leaves fp32: the activation is z or 0, its slope 1 or 0."""
+    z = torch.tensor([1e10, -1e10, 2e19, -2e19, 1e30, -1e30, 3e38, -3e38]).bfloat16()
+    z = z.repeat((I + 7) // 8)[:I]
+    x, w, gu, dh = gate_of(z, T, I)
+    one = torch.zeros_like(x)
+    one[T - 1] = x[T - 1]
+    for act in (0, 1):
+        h = nv.moe_nvfp4_gate_up(x, w, act=act).cpu()
+        assert torch.equal(h, torch.where(z > 0, z, torch.zeros_like(z)).expand(T, I))
+        _, dw = nv.moe_nvfp4_gate_up_backward(dh, one, w, gu, act=act)
+        assert torch.equal(dw[:I, 0].cpu(), (z > 0).bfloat16())
+
+
+@pytest.mark.parametrize("T,I", [(1, 8), (700, 1032)])
+def test_infinite_gates(nv, T, I):
+    """+infinity passes through; -infinity, for which z / (1 + exp(-z)) is not a number, never
+    gives a finite value but 0, and neither touches another column or row."""
+    z = torch.linspace(-3, 3, I).bfloat16()
+    x, w, _, _ = gate_of(z, T, I)
+    bad = w.clone()
+    bad[1, 0], bad[2, 0] = float("inf"), -float("inf")
+    keep = torch.ones(I, dtype=torch.bool)
+    keep[1:3] = False
+    for act in (0, 1):
+        a = nv.moe_nvfp4_gate_up(x, w, act=act).cpu()
+        b = nv.moe_nvfp4_gate_up(x, bad, act=act).cpu()
+        assert torch.equal(a[:, keep], b[:, keep])
+        assert (b[:, 1] == float("inf")).all()
+        assert (b[:, 2].isnan() | (b[:, 2] == 0)).all()
+
+
+@pytest.mark.parametrize("T,H,I", SHAPES)
+@pytest.mark.parametrize("act", [0, 1], ids=["silu", "gelu"])
+def test_no_nan_comes_of_finite_inputs(nv, T, H, I, act):
+    """Every element is written (memory that held NaN before) and is a number."""
+    x, w = (t.cuda() for t in inputs(T, H, I))
+    h, gu, dx, dw = (torch.full(s, float("nan"), dtype=torch.bfloat16, device="cuda")
+                     for s in ((T, I), (T, 2 * I), (T, H), (2 * I, H)))
+    nv.moe_nvfp4_gate_up(x, w, act=act, h=h, gu=gu)
+    nv.moe_nvfp4_gate_up_backward(h, x, w, gu, act=act, dx=dx, dw_gu=dw)
+    for t in (h, gu, dx, dw):
+        assert t.isfinite().all()
+
+
+def test_huge_up_values_beside_a_closed_gate(nv):
+    """dh u leaves fp32, dh u act'(g) is 0."""
+    z = torch.full((8,), -200.0).bfloat16()
+    x, w, gu, dh = gate_of(z, 1, 8)
+    gu[:, 8:] = 3e38
+    for act in (0, 1):
+        _, dw = nv.moe_nvfp4_gate_up_backward(4 * dh, x, w, gu, act=act)
+        assert (dw == 0).all()
