@@ -90,9 +90,16 @@ __device__ __forceinline__ void stg8(__nv_bfloat16 *p, int c, const float2 (&f)[
 struct Sum {
   static __device__ __forceinline__ float op(float a, float b) { return a + b; }
 };
+// The larger of two magnitudes.  Without a sign bit floats are ordered as their bits are, with
+// infinity and then NaN above all numbers: a row's NaN reaches its maximum.
 struct Max {
-  static __device__ __forceinline__ float op(float a, float b) { return fmaxf(a, b); }
+  static __device__ __forceinline__ float op(float a, float b) {
+    return __uint_as_float(max(__float_as_uint(a), __float_as_uint(b)));
+  }
 };
+__device__ __forceinline__ float magnitude(float v) {
+  return __uint_as_float(__float_as_uint(v) & 0x7FFFFFFFu);
+}
 
 // Reduce N values over the threads that share a row: a warp, or the CTA through `buf`
 // ([2][N][32]; the half alternates with `turn`, so one barrier a reduction is enough).  Both
@@ -166,7 +173,9 @@ __device__ __forceinline__ float code_range(float amax) {
 __device__ __forceinline__ float code_inverse(float amax, float pre) {
   return amax > 0.f ? __fdiv_rn(127.f, amax * pre) : 0.f;
 }
+// NaN for a row with NaN or an infinity, whose codes (integers) cannot say so.
 __device__ __forceinline__ float code_scale(float amax) {
+  if (!(amax < __int_as_float(0x7F800000))) return __int_as_float(0x7FC00000);
   return amax > 0.f ? __fdiv_rn(amax, 127.f) : 1.f;
 }
 
@@ -319,7 +328,7 @@ __global__ void __launch_bounds__(max_threads<MAXT>(), row_ctas(MAXT))
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             y[i][j] = mul2(mul2(y[i][j], both(r)), w[j]);
-            am[0] = fmaxf(am[0], fmaxf(fabsf(y[i][j].x), fabsf(y[i][j].y)));
+            am[0] = Max::op(am[0], Max::op(magnitude(y[i][j].x), magnitude(y[i][j].y)));
           }
         }
       } else {   // the largest of two bf16 at a time, exact
@@ -331,9 +340,9 @@ __global__ void __launch_bounds__(max_threads<MAXT>(), row_ctas(MAXT))
           const uint32_t u[4] = {xv[i].x, xv[i].y, xv[i].z, xv[i].w};
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            m = __hmax2(m, __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&u[j])));
+            m = __hmax2_nan(m, __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&u[j])));
         }
-        am[0] = fmaxf(__low2float(m), __high2float(m));
+        am[0] = Max::op(magnitude(__low2float(m)), magnitude(__high2float(m)));
       }
       reduce_row<WARP, Max>(am, buf, turn);
       const float pre = code_range(am[0]), inv = code_inverse(am[0], pre);

@@ -494,7 +494,8 @@ NVFP4_API int moe_nvfp4_gate_up_backward(const __nv_bfloat16 *dh, const __nv_bfl
  *   amax = max |x| of the row;  scale = amax / 127 (1 for an all-zero row)
  *   code = the integer nearest to 127 x / amax, ties to even (0 for an all-zero row)
  * The quotient is rounded as the real one would be, so codes are exact.  A row with NaN or
- * infinite values gets unspecified codes; other rows are not touched by it.
+ * infinite values gets unspecified codes and the scale NaN, so that its products are NaN;
+ * other rows are not touched by it.
  *   x [rows, cols] bf16    codes [rows, cols] int8    scales [rows] fp32
  * rows == 0 enqueues nothing.  Limits: cols % 16 == 0, cols <= 32768.  Alignment: x and codes
  * 16 bytes, scales 4.  Errors: EINVAL, ESHAPE, ECUDA. */

@@ -325,3 +325,27 @@ def test_pre_norm_int8_codes_are_the_nearest(nv, T, H):
     y = w.double() * x.double()
     q = 127 * y / y.abs().amax(-1, keepdim=True)
     assert ((codes.cpu().double() - q).abs() <= 0.5 + 127 * 7 * U).all()
+
+
+@pytest.mark.parametrize("H", [64, 1040, 1552, 6144, 32768])
+def test_8_bit_rows_of_nan_and_infinity_show(nv, H):
+    """A row with NaN or an infinity, and only such a row, gets the scale NaN: its products are
+    NaN, as they are without the rounding to codes."""
+    T, N = 7, 72
+    x, w = draw(1, T, H), draw(2, H, std=0.1, mean=1.0)
+    bad = x.clone()
+    bad[1, H // 3], bad[2, H - 1], bad[4, 0], bad[5] = float("nan"), float("inf"), -float("inf"), 0
+    bad[6] = float("nan")
+    wq = torch.randint(-127, 128, (N, H), generator=torch.Generator().manual_seed(3),
+                       dtype=torch.int8).cuda()
+    ws = torch.ones(N, device="cuda")
+    for rows in (nv.nvfp4_int8_quantize, lambda t: nv.moe_nvfp4_pre_norm_int8(t, w.cuda(), EPS)):
+        cc, cs = rows(x.cuda())
+        bc, bs = rows(bad.cuda())
+        for t in (0, 3):
+            assert torch.equal(bc[t], cc[t]) and bs[t] == cs[t]
+        assert (bc[5] == 0).all() and bs[5] == 1
+        out = nv.nvfp4_int8_matmul(bc, bs, wq, ws)
+        for t in (1, 2, 4, 6):
+            assert bs[t].isnan() and out[t].isnan().all(), t
+        assert out[[0, 3, 5]].isfinite().all()
