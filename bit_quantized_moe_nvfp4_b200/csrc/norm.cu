@@ -83,6 +83,10 @@ __device__ __forceinline__ uint4 pack8(const float2 (&f)[4]) {
 __device__ __forceinline__ uint4 ldg8(const __nv_bfloat16 *p, int c) {
   return __ldg(reinterpret_cast<const uint4 *>(p) + c);
 }
+// An ordinary load, which stores that follow it may overwrite.
+__device__ __forceinline__ uint4 ld8(const __nv_bfloat16 *p, int c) {
+  return reinterpret_cast<const uint4 *>(p)[c];
+}
 __device__ __forceinline__ void stg8(__nv_bfloat16 *p, int c, const float2 (&f)[4]) {
   reinterpret_cast<uint4 *>(p)[c] = pack8(f);
 }
@@ -374,7 +378,7 @@ __global__ void __launch_bounds__(max_threads<MAXT>(), row_ctas(MAXT))
         unpack8(ldg8(p.w, c), w);
         if (p.gh) {   // a gate for each value is a third row array
           float2 g[4];
-          unpack8(p.gt ? feed.get(at, 2, i) : ldg8(p.gate, c), g);
+          unpack8(p.gt ? feed.get(at, 2, i) : ld8(p.gate, c), g);
 #pragma unroll
           for (int j = 0; j < 4; ++j) w[j] = mul2(w[j], g[j]);
         }
@@ -471,7 +475,7 @@ __global__ void __launch_bounds__(max_threads<MAXT>(), grad_row_ctas(MAXT, VPT, 
       unpack8(ldg8(p.w, c), w);
       if (GATE >= kChannelGate) {
         float2 g[4];
-        unpack8(GATE == kFullGate ? feed.get(at, 2, i) : ldg8(p.gate, c), g);
+        unpack8(GATE == kFullGate ? feed.get(at, 2, i) : ld8(p.gate, c), g);
 #pragma unroll
         for (int j = 0; j < 4; ++j) w[j] = mul2(w[j], g[j]);
       }
@@ -501,6 +505,9 @@ __global__ void __launch_bounds__(max_threads<MAXT>(), grad_row_ctas(MAXT, VPT, 
       unpack8(feed.get(at, 0, i), x);   // read again: registers hold the column sums
       unpack8(feed.get(at, 1, i), d);
       unpack8(ldg8(p.w, c), w);
+      float2 g[4];   // before the stores: of one row, any output may be the gate's tensor
+      if (GATE >= kChannelGate)
+        unpack8(GATE == kFullGate ? feed.get(at, 2, i) : ld8(p.gate, c), g);
       if (p.dres) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) o[j] = mul2(d[j], both(p.a));
@@ -510,8 +517,6 @@ __global__ void __launch_bounds__(max_threads<MAXT>(), grad_row_ctas(MAXT, VPT, 
 #pragma unroll
       for (int j = 0; j < 4; ++j) n[j] = mul2(x[j], both(rg));
       if (GATE >= kChannelGate) {
-        float2 g[4];
-        unpack8(GATE == kFullGate ? feed.get(at, 2, i) : ldg8(p.gate, c), g);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const float2 dw = mul2(d[j], w[j]);

@@ -349,3 +349,21 @@ def test_8_bit_rows_of_nan_and_infinity_show(nv, H):
         for t in (1, 2, 4, 6):
             assert bs[t].isnan() and out[t].isnan().all(), t
         assert out[[0, 3, 5]].isfinite().all()
+
+
+@pytest.mark.parametrize("H", [264, 2056, 6144, 16384])
+def test_in_place_one_row(nv, H):
+    """With one row, a channel gate has the shape of the rows: every output may be its tensor."""
+    y, d, w, g = (draw(k, 1, H).cuda() for k in range(4))
+    w = w[0].contiguous()
+    want = nv.moe_nvfp4_post_norm_backward(d, y, w, EPS, gate=g, residual_scale=0.5)
+    for name in ("dresidual", "dy", "dgate"):
+        a = g.clone()
+        got = nv.moe_nvfp4_post_norm_backward(d, y, w, EPS, gate=a, residual_scale=0.5,
+                                              **{name: a})
+        assert all(torch.equal(p, q) for p, q in zip(got, want)), name
+    want = nv.moe_nvfp4_post_norm(y, w, d, EPS, gate=g, next_weight=w)
+    for name in ("out", "next_out"):
+        a = g.clone()
+        got = nv.moe_nvfp4_post_norm(y, w, d, EPS, gate=a, next_weight=w, **{name: a})
+        assert all(torch.equal(p, q) for p, q in zip(got, want)), name
