@@ -489,7 +489,9 @@ __global__ void __launch_bounds__(max_threads<MAXT>(), grad_row_ctas(MAXT, VPT, 
     reduce_row<WARP, Sum>(s, buf, turn);
     const float r = rsqrtf(fmaf(s[0], inv_h, p.eps));
     const float rg = r * g1;
-    const float k = rg * r * (r * s[1] * inv_h);   // r mean(dn n) r: dx = r dn - k x
+    // dx = r dn - r mean(dn n) n; both terms carry the row's single gate, the second in x rg.
+    // No product here holds r^2 alone, which leaves fp32 at the smallest eps.
+    const float rm = r * (r * s[1] * inv_h);
     if (GATE == kRowGate) {
       if (p.sum_g == 2)
         a1 += r * s[1];
@@ -537,7 +539,7 @@ __global__ void __launch_bounds__(max_threads<MAXT>(), grad_row_ctas(MAXT, VPT, 
         for (int j = 0; j < 4; ++j) o[j] = mul2(mul2(d[j], w[j]), both(rg));
       }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) o[j] = fma2(x[j], both(-k), o[j]);
+      for (int j = 0; j < 4; ++j) o[j] = fma2(n[j], both(-rm), o[j]);
       stg8(p.dx + row, c, o);
     }
     feed.fetch(t + rows.stages * step, at);

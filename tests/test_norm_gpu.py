@@ -7,6 +7,8 @@ most 32 warps, so it is off by < 80 u; r = rsqrt is off by half of that and 4 u 
 weight, the gate and the sum add < 8 u.  Every fp32 value before the last rounding is then
 within E = 2^-17 = 128 u of the sum of the magnitudes of its terms.  A sum over T rows adds
 T u of its terms' magnitudes."""
+import functools
+
 import numpy as np
 import pytest
 import torch
@@ -367,3 +369,36 @@ def test_in_place_one_row(nv, H):
         a = g.clone()
         got = nv.moe_nvfp4_post_norm(y, w, d, EPS, gate=a, next_weight=w, **{name: a})
         assert all(torch.equal(p, q) for p, q in zip(got, want)), name
+
+
+@pytest.fixture
+def no_nan(monkeypatch):
+    """The comparisons of this module refuse NaN."""
+    monkeypatch.setitem(globals(), "close", functools.partial(_no_nan, close))
+
+
+def _no_nan(compare, got, ref, slack):
+    assert not got.isnan().any()
+    compare(got, ref, slack)
+
+
+@pytest.mark.parametrize("H", [64, 2056, 6144])
+def test_smallest_eps(nv, no_nan, H):
+    """eps below fp32's normal range: rows of zeros give zeros and finite gradients, 1 / sqrt(eps)
+    times the gradient of the normed row."""
+    eps = 2.0 ** -130
+    x, d, w = draw(1, 4, H), draw(2, 4, H, std=0.1), draw(3, H, std=0.1, mean=1.0)
+    x[1] = 0
+    g = draw(4, 4, 1, std=0.5, mean=0.5)
+    assert (nv.moe_nvfp4_pre_norm(x.cuda(), w.cuda(), eps)[1] == 0).all()
+    dx, _ = nv.moe_nvfp4_pre_norm_backward(d.cuda(), x.cuda(), w.cuda(), eps)
+    dy, _, dg, _ = nv.moe_nvfp4_post_norm_backward(d.cuda(), x.cuda(), w.cuda(), eps,
+                                                   gate=g.cuda())
+    ref = 2.0 ** 65 * d[1].double() * w.double()
+    close(dx[1], ref, E * ref.abs())
+    ref = ref * g[1].double()
+    close(dy[1], ref, E * ref.abs())
+    assert dg[1] == 0
+    # the other rows: eps is nothing beside mean(x^2)
+    rx, rm, *_ = grads(x[[0, 2, 3]], w, None, d[[0, 2, 3]], 1.0)
+    close(dx[[0, 2, 3]], rx, 2 * (E + EPS) * rm)
