@@ -23,7 +23,8 @@ __all__ = [
     "nvfp4_quantize", "nvfp4_quantize_workspace_size", "nvfp4_dequantize", "nvfp4_cast_f32",
     "moe_nvfp4_route", "moe_nvfp4_workspace_size", "moe_nvfp4_forward",
     "moe_nvfp4_read_error_flag", "moe_nvfp4_forward_profiled", "alloc_moe_workspace",
-    "moe_nvfp4_forward_static", "nvfp4_selftest_wait_timeout", "nvfp4_amax",
+    "moe_nvfp4_forward_static", "nvfp4_selftest_wait_timeout",
+    "nvfp4_selftest_gate_up_timeout", "nvfp4_selftest_int8_matmul_timeout", "nvfp4_amax",
     "nvfp4_quantize_with_amax", "moe_nvfp4_ep_local_experts", "moe_nvfp4_forward_ep",
     "moe_nvfp4_ep_reduce", "EP_MAX_PARTS", "moe_nvfp4_router", "moe_nvfp4_forward_logits",
     "moe_nvfp4_shared_expert", "moe_nvfp4_layer", "moe_nvfp4_layer_workspace_size",
@@ -97,6 +98,8 @@ def _load() -> ctypes.CDLL:
         "moe_nvfp4_gate_up": (I32, [P, P, I64, I64, I64, I32, P, P, P, P]),
         "moe_nvfp4_gate_up_backward_workspace_size": (SZ, [I64, I64]),
         "moe_nvfp4_gate_up_backward": (I32, [P, P, P, P, I64, I64, I64, I32, P, P, P, SZ, P, P]),
+        "nvfp4_selftest_gate_up_timeout": (I32, [P, P, I64, I64, I64, P, P, P, P]),
+        "nvfp4_selftest_int8_matmul_timeout": (I32, [P, P, P, P, I64, I64, I64, P, P, P]),
         "nvfp4_int8_quantize": (I32, [P, I64, I64, P, P, P]),
         "nvfp4_int8_matmul": (I32, [P, P, P, P, I64, I64, I64, P, P, P]),
         "moe_nvfp4_shared_workspace_size": (SZ, [I64, I64]),
@@ -860,6 +863,28 @@ def nvfp4_selftest_wait_timeout(flag: torch.Tensor, kind: int, limit_ns: int) ->
         raise ValueError("flag: expected a CUDA tensor")
     _check(_lib().nvfp4_selftest_wait_timeout(_ptr(flag), int(kind), int(limit_ns),
                                               _stream(flag.device)))
+
+
+def nvfp4_selftest_gate_up_timeout(x, w_gu, h, gu, error_flag) -> None:
+    """Test hook: moe_nvfp4_gate_up (SiLU) with loads that never come and waits of 2 ms; bit 1 of
+    error_flag is set and h and gu (or None) are NaN where they could not be computed."""
+    bf = torch.bfloat16
+    T, H, dev, px = _matrix(x, bf, "x")
+    I, pw = _gate_up_rows(w_gu, H, dev)
+    ph, pgu = _arg(h, bf, (T, I), dev, "h"), _optional(gu, bf, (T, 2 * I), dev, "gu")
+    _check(_lib().nvfp4_selftest_gate_up_timeout(px, pw, T, H, I, ph, pgu, _flag(error_flag, dev),
+                                                 _stream(x.device)))
+
+
+def nvfp4_selftest_int8_matmul_timeout(a, a_scales, w, w_scales, out, error_flag) -> None:
+    """Test hook: nvfp4_int8_matmul in the same way."""
+    T, K, dev, pa = _matrix(a, torch.int8, "a")
+    N, pw = _weight(w, torch.int8, K, dev, "w")
+    pas = _arg(a_scales, torch.float32, (T,), dev, "a_scales")
+    pws = _arg(w_scales, torch.float32, (N,), dev, "w_scales")
+    po = _arg(out, torch.bfloat16, (T, N), dev, "out")
+    _check(_lib().nvfp4_selftest_int8_matmul_timeout(pa, pas, pw, pws, T, N, K, po,
+                                                     _flag(error_flag, dev), _stream(a.device)))
 
 
 def moe_nvfp4_read_error_flag(workspace: torch.Tensor) -> int:

@@ -20,7 +20,9 @@
 //    Bound by the stream of weights at few tokens (1 x 4096 x 6144 bf16: 11.2 us for 50 MB),
 //    by the parts' way between the SMs at 64 (1.5 to 2 us of 10 at 64 x 4096 x 6144, 8-bit).
 //
-// Every wait is bounded; one that gives up ORs bit 1 into the caller's error flag.
+// Every wait is bounded.  One that gives up ORs bit 1 into the caller's error flag, nothing is
+// issued or re-armed behind it, and what it was waiting for comes out as NaN: a lost tile shows
+// without a flag too.  (LOSE: the selftest kernels, which leave out loads and wait 2 ms.)
 #pragma once
 #include <algorithm>
 
@@ -64,10 +66,11 @@ struct DenseArgs {
 struct CtaWait {
   int *abort;
   int32_t *flag;
+  uint64_t limit_ns;
   __device__ __forceinline__ bool operator()(uint64_t *bar, uint32_t parity) const {
     if (mbar_try_wait(bar, parity)) return true;
     if (*(volatile int *)abort) return false;
-    if (mbar_wait(bar, parity)) return true;
+    if (mbar_wait(bar, parity, limit_ns)) return true;
     *(volatile int *)abort = 1;
     report_timeout(flag);
     return false;
@@ -88,6 +91,14 @@ __device__ __forceinline__ bool elect_one() {
                : "=r"(p));
   return p != 0;
 }
+
+template <bool LOSE>
+constexpr uint64_t wait_limit() {
+  return LOSE ? 2000000ull : kWaitLimitNs;
+}
+// What a lost value is: two bf16 NaN, an fp32 NaN, and in the int32 sums (|sum| <= 2^29) the
+// lowest value.
+constexpr uint32_t kLostBf16x2 = 0x7FFF7FFFu, kLostF32 = 0x7FFFFFFFu, kLostS32 = 0x80000000u;
 
 // ------------------------------------------------------------------ pairs of CTAs
 constexpr int kPS = 6;                              // stages
@@ -147,7 +158,7 @@ __device__ __forceinline__ void store_chunk(const uint32_t (&v)[32], unsigned ch
   }
 }
 
-template <int KIND, bool AMN, bool BMN, int EPI, int ACT>
+template <int KIND, bool AMN, bool BMN, int EPI, int ACT, bool LOSE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
     dense_pair_kernel(const __grid_constant__ CUtensorMap map_a,
                       const __grid_constant__ CUtensorMap map_b,
@@ -189,7 +200,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
   const uint32_t tmem_base = *tmem_slot;
   pdl_wait();
 
-  const CtaWait wait{abort, p.flag};
+  const CtaWait wait{abort, p.flag, wait_limit<LOSE>()};
   const int total = p.items, pairs = (int)gridDim.x / 2;
   const int first = (int)blockIdx.x / 2;
   constexpr int kElems = KIND == kS8 ? 128 : 64;   // K elements of a stage
@@ -214,13 +225,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
           const uint32_t bar = full0 + s * 8;
           unsigned char *A = smem + s * kPStage, *B = A + kPHalf;
           const int k0 = kb * kElems;
-          if (AMN) {
+          if (LOSE && rank == 1 && i != first && kb == 0) {
+            // the peer's part of a pair's second tile never lands
+          } else if (AMN) {
             tma_load_2d_pair(A, &map_a, m0, k0, bar);
             tma_load_2d_pair(A + kPHalf / 2, &map_a, m0 + 64, k0, bar);
           } else {
             tma_load_2d_pair(A, &map_a, k0, m0, bar);
           }
-          if (BMN) {
+          if (LOSE && rank == 1 && i != first && kb == 0) {
+          } else if (BMN) {
             tma_load_2d_pair(B, &map_b, n0, k0, bar);
             if (hw > 64) tma_load_2d_pair(B + kPHalf / 2, &map_b, n0 + 64, k0, bar);
           } else {
@@ -233,10 +247,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
     }
     // the leader sees both CTAs' copies land; the peer stays until then (cluster_sync)
     if (rank == 0)
-      for (int t = max(0, kg - kPS); t < kg; ++t) mbar_wait(&full[t % kPS], (t / kPS) & 1);
+      for (int t = max(0, kg - kPS); t < kg; ++t)
+        mbar_wait(&full[t % kPS], (t / kPS) & 1, wait_limit<LOSE>());
   } else if (warp == 1) {
     if (rank == 0) {
       int kg = 0, tc = 0;
+      bool ok = true;
       for (int i = first; i < total; i += pairs, ++tc) {
         const int acc = tc & 1;
         if (tc >= 2 && !wait.warp(&accempty[acc], ((tc >> 1) - 1) & 1)) break;
@@ -248,28 +264,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
             (AMN ? kIdescMnMajorA : 0) | (BMN ? kIdescMnMajorB : 0);
         for (int kb = 0; kb < kblocks; ++kb, ++kg) {
           const int s = kg % kPS;
-          const bool ok = wait.warp(&full[s], (kg / kPS) & 1);
+          ok = wait.warp(&full[s], (kg / kPS) & 1);
+          if (!ok) break;   // nothing is committed: the others give up in their turn
           tc_fence_after();
           if (elect_one()) {
-            if (ok) {
-              const uint32_t a = smem_u32(smem + s * kPStage);
-              const uint64_t da = AMN ? smem_desc_mn_sw128(a, kPHalf / 2) : smem_desc_sw128(a);
-              const uint64_t db = BMN ? smem_desc_mn_sw128(a + kPHalf, kPHalf / 2)
-                                      : smem_desc_sw128(a + kPHalf);
+            const uint32_t a = smem_u32(smem + s * kPStage);
+            const uint64_t da = AMN ? smem_desc_mn_sw128(a, kPHalf / 2) : smem_desc_sw128(a);
+            const uint64_t db = BMN ? smem_desc_mn_sw128(a + kPHalf, kPHalf / 2)
+                                    : smem_desc_sw128(a + kPHalf);
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk) {
-                // 32 bytes along the rows (K-major), or 16 K rows of 128 bytes (MN-major)
-                const uint64_t ak = da + (AMN ? 128 : 2) * kk, bk = db + (BMN ? 128 : 2) * kk;
-                if (KIND == kS8)
-                  umma_s8_pair(d, ak, bk, idesc, kb > 0 || kk > 0);
-                else
-                  umma_bf16_pair(d, ak, bk, idesc, kb > 0 || kk > 0);
-              }
+            for (int kk = 0; kk < 4; ++kk) {
+              // 32 bytes along the rows (K-major), or 16 K rows of 128 bytes (MN-major)
+              const uint64_t ak = da + (AMN ? 128 : 2) * kk, bk = db + (BMN ? 128 : 2) * kk;
+              if (KIND == kS8)
+                umma_s8_pair(d, ak, bk, idesc, kb > 0 || kk > 0);
+              else
+                umma_bf16_pair(d, ak, bk, idesc, kb > 0 || kk > 0);
             }
             umma_commit_pair(&freeb[s]);
           }
           __syncwarp();
         }
+        if (!ok) break;
         if (elect_one()) umma_commit_pair(&accfull[acc]);
         __syncwarp();
       }
@@ -278,15 +294,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
     const int q = warp & 3;
     unsigned char *buf = smem + kPOut + (warp - 2) * 8192;
     int tc = 0, nst = 0;
+    bool lost = false;   // stays: the barriers' phases mean nothing behind a lost tile
     for (int i = first; i < total; i += pairs, ++tc) {
       const PairItem it = item_at(i, p);
       const int hw = it.width / 2;
       const int acc = tc & 1;
-      if (!wait.warp(&accfull[acc], (tc >> 1) & 1)) break;
+      lost = lost || !wait.warp(&accfull[acc], (tc >> 1) & 1);
       tc_fence_after();
       const uint32_t tb = tmem_base + acc * 256 + ((uint32_t)(q * 32) << 16);
       const int row0 = it.mt * 256 + rank * 128 + q * 32;
       const bool rows_in = row0 < p.M;
+      if (lost) {
+        uint32_t bad[32];
+#pragma unroll
+        for (int k = 0; k < 32; ++k) bad[k] = kLostBf16x2;
+        const int cols = EPI == kEpiGate ? hw : it.width;
+        for (int c = 0; c < cols / 64; ++c) {
+          const int x = it.nt * (EPI == kEpiGate ? 128 : 256) + it.part * cols + c * 64;
+          const bool in = rows_in && x < p.N;
+          store_chunk(bad, buf + (nst++ & 1) * 4096, lane, &map_out, x, row0, in);
+          if (EPI == kEpiGate && p.save_gu) {
+            store_chunk(bad, buf + (nst++ & 1) * 4096, lane, &map_g, x, row0, in);
+            store_chunk(bad, buf + (nst++ & 1) * 4096, lane, &map_u, x, row0, in);
+          }
+        }
+        continue;
+      }
       if (EPI == kEpiGate) {
         // the first half of the columns is the gate, the second the up projection of the
         // same columns of h
@@ -393,7 +426,7 @@ __device__ __forceinline__ uint2 pack4(float4 v) {
   return make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
 }
 
-template <int KIND, bool AMN, bool BMN, int EPI, int ACT, int NT, bool ROWS>
+template <int KIND, bool AMN, bool BMN, int EPI, int ACT, int NT, bool ROWS, bool LOSE>
 __global__ void __launch_bounds__(kSThreads, 2)
     dense_split_kernel(const __grid_constant__ CUtensorMap map_a,
                        const __grid_constant__ CUtensorMap map_b, DenseArgs p) {
@@ -408,7 +441,7 @@ __global__ void __launch_bounds__(kSThreads, 2)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)cluster_rank(), nr = (int)cluster_size();
 
-  const CtaWait wait{abort, p.flag};
+  const CtaWait wait{abort, p.flag, wait_limit<LOSE>()};
   constexpr int kElems = KIND == kS8 ? 128 : 64;
   const int kblocks = (int)((p.K + kElems - 1) / kElems);
   const int kb0 = (int)((int64_t)rank * kblocks / nr), kb1 = (int)((int64_t)(rank + 1) * kblocks / nr);
@@ -465,7 +498,9 @@ __global__ void __launch_bounds__(kSThreads, 2)
         mbar_arrive_expect_tx(&full[s], S::kStage);
         unsigned char *A = smem + s * S::kStage, *B = A + S::kA;
         const int k0 = kb * kElems;
-        if (EPI == kEpiGate) {   // 64 gate rows, then the matching 64 up rows
+        if (LOSE && rank == 0 && i == 0) {
+          // the first CTA's first weights never land
+        } else if (EPI == kEpiGate) {   // 64 gate rows, then the matching 64 up rows
           tma_load_2d(A, &map_a, k0, m0, &full[s]);
           tma_load_2d(A + S::kA / 2, &map_a, k0, (int)p.half + m0, &full[s]);
         } else if (AMN) {
@@ -486,40 +521,41 @@ __global__ void __launch_bounds__(kSThreads, 2)
     }
     // every copy lands before the ring is used again or the CTA exits
     for (int t = max(0, i - S::kStages); t < i; ++t)
-      mbar_wait(&full[t % S::kStages], (t / S::kStages) & 1);
+      mbar_wait(&full[t % S::kStages], (t / S::kStages) & 1, wait_limit<LOSE>());
   } else if (warp == 1) {
     const uint32_t tmem_base = *tmem_slot;
     constexpr uint32_t idesc = (KIND == kS8 ? idesc_s8_s32(128, NT) : idesc_bf16_f32(128, NT)) |
                                (AMN ? kIdescMnMajorA : 0) | (BMN ? kIdescMnMajorB : 0);
+    bool ok = true;
     for (int i = 0; i < kb1 - kb0; ++i) {
       const int s = i % S::kStages;
-      const bool ok = wait.warp(&full[s], (i / S::kStages) & 1);
+      ok = wait.warp(&full[s], (i / S::kStages) & 1);
+      if (!ok) break;   // nothing is committed: the others give up in their turn
       tc_fence_after();
       if (elect_one()) {
-        if (ok) {
-          const uint32_t a = smem_u32(smem + s * S::kStage);
-          const uint64_t da = AMN ? smem_desc_mn_sw128(a, S::kA / 2) : smem_desc_sw128(a);
-          const uint64_t db =
-              BMN ? smem_desc_mn_sw128(a + S::kA, 8192) : smem_desc_sw128(a + S::kA);
+        const uint32_t a = smem_u32(smem + s * S::kStage);
+        const uint64_t da = AMN ? smem_desc_mn_sw128(a, S::kA / 2) : smem_desc_sw128(a);
+        const uint64_t db =
+            BMN ? smem_desc_mn_sw128(a + S::kA, 8192) : smem_desc_sw128(a + S::kA);
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            const uint64_t ak = da + (AMN ? 128 : 2) * kk, bk = db + (BMN ? 128 : 2) * kk;
-            if (KIND == kS8)
-              umma_s8(tmem_base, ak, bk, idesc, i > 0 || kk > 0);
-            else
-              umma_bf16(tmem_base, ak, bk, idesc, i > 0 || kk > 0);
-          }
+        for (int kk = 0; kk < 4; ++kk) {
+          const uint64_t ak = da + (AMN ? 128 : 2) * kk, bk = db + (BMN ? 128 : 2) * kk;
+          if (KIND == kS8)
+            umma_s8(tmem_base, ak, bk, idesc, i > 0 || kk > 0);
+          else
+            umma_bf16(tmem_base, ak, bk, idesc, i > 0 || kk > 0);
         }
         umma_commit(&freeb[s]);
       }
       __syncwarp();
     }
-    if (elect_one()) umma_commit(accfull);
+    if (ok && elect_one()) umma_commit(accfull);
   }
   __syncwarp();
   // every thread of the CTA waits for the tile: the ring is free and may hold partial sums
-  const bool done = wait(accfull, 0);
+  wait(accfull, 0);
   __syncthreads();   // the producer's copies have landed too
+  const bool lost = *(volatile int *)abort;   // a wait of this CTA gave up: its part is not there
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   uint32_t *red = reinterpret_cast<uint32_t *>(smem);
@@ -527,14 +563,13 @@ __global__ void __launch_bounds__(kSThreads, 2)
   {   // two warps for each quarter of the TMEM lanes, 16 columns at a time in turn
     const int row = (warp & 3) * 32 + lane;
     const uint32_t tb = tmem_base + ((uint32_t)((warp & 3) * 32) << 16);
-    const bool any = done && kb1 > kb0;
 #pragma unroll 1
     for (int c = (warp >> 2) * 16; c < ncols; c += 32) {
       uint32_t v[16];
       tmem_ld16(tb + c, v);
-      if (!any)
+      if (lost)
 #pragma unroll
-        for (int k = 0; k < 16; ++k) v[k] = 0;
+        for (int k = 0; k < 16; ++k) v[k] = KIND == kS8 ? kLostS32 : kLostF32;
       if (ROWS) {
 #pragma unroll
         for (int k = 0; k < 16; k += 4)
@@ -565,12 +600,15 @@ __global__ void __launch_bounds__(kSThreads, 2)
     float4 v = w[0];
     if (KIND == kS8) {   // an absent part is 0 in either type
       int a[4] = {0, 0, 0, 0};
+      bool gone = false;
 #pragma unroll
       for (int r = 0; r < kMaxSplit; ++r) {
+        gone = gone || __float_as_uint(w[r].x) == kLostS32;
         a[0] += __float_as_int(w[r].x), a[1] += __float_as_int(w[r].y);
         a[2] += __float_as_int(w[r].z), a[3] += __float_as_int(w[r].w);
       }
       v = make_float4((float)a[0], (float)a[1], (float)a[2], (float)a[3]);
+      if (gone) v.x = v.y = v.z = v.w = __uint_as_float(kLostF32);
     } else {
 #pragma unroll
       for (int r = 1; r < kMaxSplit; ++r)
@@ -653,7 +691,7 @@ struct DenseOperands {
   const void *a, *b;
 };
 
-template <int KIND, bool AMN, bool BMN, int EPI, int ACT>
+template <int KIND, bool AMN, bool BMN, int EPI, int ACT, bool LOSE = false>
 int launch_pair(DenseArgs p, DenseOperands o, const CUtensorMap &out, const CUtensorMap &g,
                 const CUtensorMap &u, cudaStream_t s) {
   CUtensorMap ta, tb;
@@ -662,7 +700,7 @@ int launch_pair(DenseArgs p, DenseOperands o, const CUtensorMap &out, const CUte
   if (int st = operand_map(&tb, KIND, BMN, o.b, brows, p.K, 64)) return st;
   p.m_tiles = (int)ceil_div(p.M, 256);
   p.n_tiles = (int)ceil_div(p.N, EPI == kEpiGate ? 128 : 256);
-  auto k = dense_pair_kernel<KIND, AMN, BMN, EPI, ACT>;
+  auto k = dense_pair_kernel<KIND, AMN, BMN, EPI, ACT, LOSE>;
   if (resident_blocks(k, kPThreads, kPSmem) < 0) return NVFP4_ECUDA;
   const int total = p.m_tiles * p.n_tiles, slots = num_sms() / 2;
   const int left = total % slots;
@@ -693,7 +731,8 @@ inline int split_count(int64_t tiles, int64_t kblocks, size_t smem) {
   return 1;
 }
 
-template <int KIND, bool AMN, bool BMN, int EPI, int ACT, int NT, bool ROWS = false>
+template <int KIND, bool AMN, bool BMN, int EPI, int ACT, int NT, bool ROWS = false,
+          bool LOSE = false>
 int launch_split(DenseArgs p, DenseOperands o, cudaStream_t s) {
   using S = SplitShape<NT, ROWS>;
   CUtensorMap ta, tb;
@@ -702,7 +741,7 @@ int launch_split(DenseArgs p, DenseOperands o, cudaStream_t s) {
   if (int st = operand_map(&tb, KIND, BMN, o.b, p.N, p.K, NT)) return st;
   p.m_tiles = (int)ceil_div(p.M, EPI == kEpiGate ? 64 : 128);
   p.n_tiles = (int)ceil_div(p.N, NT);
-  auto k = dense_split_kernel<KIND, AMN, BMN, EPI, ACT, NT, ROWS>;
+  auto k = dense_split_kernel<KIND, AMN, BMN, EPI, ACT, NT, ROWS, LOSE>;
   if (resident_blocks(k, kSThreads, S::kSmem) <= 0) return NVFP4_ECUDA;
   const int64_t tiles = (int64_t)p.m_tiles * p.n_tiles;
   const int64_t kblocks = ceil_div(p.K, KIND == kS8 ? 128 : 64);
@@ -734,11 +773,11 @@ int launch_split(DenseArgs p, DenseOperands o, cudaStream_t s) {
 // partial tiles' way through the cluster costs more than the second read of A it saves (8-bit
 // 128 x 4096 x 1024 with its quantizer: 9.8 us against 11.7; it won by 8% at 192..256 x 6144
 // x 4096).
-template <int KIND, bool AMN, int EPI, int ACT>
+template <int KIND, bool AMN, int EPI, int ACT, bool LOSE = false>
 int launch_split_n(const DenseArgs &p, DenseOperands o, cudaStream_t s) {
-  if (p.N <= 16) return launch_split<KIND, AMN, false, EPI, ACT, 16>(p, o, s);
-  if (p.N <= 32) return launch_split<KIND, AMN, false, EPI, ACT, 32>(p, o, s);
-  return launch_split<KIND, AMN, false, EPI, ACT, 64>(p, o, s);
+  if (p.N <= 16) return launch_split<KIND, AMN, false, EPI, ACT, 16, false, LOSE>(p, o, s);
+  if (p.N <= 32) return launch_split<KIND, AMN, false, EPI, ACT, 32, false, LOSE>(p, o, s);
+  return launch_split<KIND, AMN, false, EPI, ACT, 64, false, LOSE>(p, o, s);
 }
 
 }  // namespace nvfp4

@@ -70,7 +70,7 @@ __global__ void __launch_bounds__(256) gate_grad_kernel(const __nv_bfloat16 *gu,
   }
 }
 
-template <int ACT>
+template <int ACT, bool LOSE = false>
 int forward(const __nv_bfloat16 *x, const __nv_bfloat16 *w_gu, int64_t T, int64_t H, int64_t I,
             __nv_bfloat16 *h, __nv_bfloat16 *gu, int32_t *flag, cudaStream_t s) {
   DenseArgs p = {};
@@ -84,10 +84,10 @@ int forward(const __nv_bfloat16 *x, const __nv_bfloat16 *w_gu, int64_t T, int64_
       if (int st = out_map(&tg, gu, T, I, 2 * I)) return st;
       if (int st = out_map(&tu, gu + I, T, I, 2 * I)) return st;
     }
-    return launch_pair<kBf16, false, false, kEpiGate, ACT>(p, {x, w_gu}, th, tg, tu, s);
+    return launch_pair<kBf16, false, false, kEpiGate, ACT, LOSE>(p, {x, w_gu}, th, tg, tu, s);
   }
   p.M = I, p.N = T;
-  return launch_split_n<kBf16, false, kEpiGate, ACT>(p, {w_gu, x}, s);
+  return launch_split_n<kBf16, false, kEpiGate, ACT, LOSE>(p, {w_gu, x}, s);
 }
 
 int check(int64_t T, int64_t H, int64_t I, int act) {
@@ -96,6 +96,17 @@ int check(int64_t T, int64_t H, int64_t I, int act) {
   if (H % 8 || I % 8 || H > 65536 || I > 65536 || T >= (int64_t(1) << 30) ||
       T > (int64_t(1) << 44) / std::max(H, 2 * I))
     return NVFP4_ESHAPE;
+  return NVFP4_OK;
+}
+
+int check_forward(const __nv_bfloat16 *x, const __nv_bfloat16 *w_gu, int64_t T, int64_t H,
+                  int64_t I, int act, const __nv_bfloat16 *h, const __nv_bfloat16 *gu,
+                  const int32_t *error_flag) {
+  if (int st = check(T, H, I, act)) return st;
+  if (!w_gu || !aligned16(w_gu) || (reinterpret_cast<uintptr_t>(error_flag) & 3))
+    return NVFP4_EINVAL;
+  if (T > 0 && (!x || !h || !aligned16(x) || !aligned16(h) || !aligned16(gu)))
+    return NVFP4_EINVAL;
   return NVFP4_OK;
 }
 
@@ -114,13 +125,19 @@ using namespace nvfp4;
 extern "C" int moe_nvfp4_gate_up(const __nv_bfloat16 *x, const __nv_bfloat16 *w_gu, int64_t T,
                                  int64_t H, int64_t I, int act, __nv_bfloat16 *h,
                                  __nv_bfloat16 *gu, int32_t *error_flag, cudaStream_t stream) {
-  if (int st = check(T, H, I, act)) return st;
-  if (!w_gu || !aligned16(w_gu) || (reinterpret_cast<uintptr_t>(error_flag) & 3))
-    return NVFP4_EINVAL;
+  if (int st = check_forward(x, w_gu, T, H, I, act, h, gu, error_flag)) return st;
   if (T == 0) return NVFP4_OK;
-  if (!x || !h || !aligned16(x) || !aligned16(h) || !aligned16(gu)) return NVFP4_EINVAL;
   return act == NVFP4_ACT_SILU ? forward<NVFP4_ACT_SILU>(x, w_gu, T, H, I, h, gu, error_flag, stream)
                                : forward<NVFP4_ACT_GELU>(x, w_gu, T, H, I, h, gu, error_flag, stream);
+}
+
+extern "C" int nvfp4_selftest_gate_up_timeout(const __nv_bfloat16 *x, const __nv_bfloat16 *w_gu,
+                                              int64_t T, int64_t H, int64_t I, __nv_bfloat16 *h,
+                                              __nv_bfloat16 *gu, int32_t *error_flag,
+                                              cudaStream_t stream) {
+  if (int st = check_forward(x, w_gu, T, H, I, NVFP4_ACT_SILU, h, gu, error_flag)) return st;
+  if (T == 0 || !error_flag) return NVFP4_EINVAL;
+  return forward<NVFP4_ACT_SILU, true>(x, w_gu, T, H, I, h, gu, error_flag, stream);
 }
 
 extern "C" size_t moe_nvfp4_gate_up_backward_workspace_size(int64_t T, int64_t I) {

@@ -462,8 +462,9 @@ NVFP4_API int moe_nvfp4_post_norm_backward(
  *   gu = bf16( [g | u] )        kept for the gradients when not NULL
  *   x [T, H] bf16   w_gu [2I, H] bf16 (gate rows, then up rows)   h [T, I] bf16
  *   gu [T, 2I] bf16 or NULL      act NVFP4_ACT_*
- * error_flag: [1] int32, device, may be NULL: bit 1 is ORed in if a device-side wait gave up
- * (the outputs are then invalid); nothing else is written, so the caller zeroes it once.
+ * error_flag: [1] int32, device, may be NULL: bit 1 is ORed in if a device-side wait gave up;
+ * nothing else is written, so the caller zeroes it once.  The results that then could not be
+ * computed are NaN, with or without a flag.
  * No workspace.  T == 0 enqueues nothing.
  * Limits: H % 8 == 0, I % 8 == 0, H and I <= 65536, T < 2^30, T max(H, 2I) <= 2^44.
  * Alignment: 16 bytes (error_flag 4).  Outputs must not overlap inputs.  Errors: EINVAL, ESHAPE, ECUDA. */
@@ -566,6 +567,21 @@ NVFP4_API int moe_nvfp4_forward_static(const __nv_bfloat16 *x, const int32_t *to
  * 1..1000000000), ECUDA. */
 NVFP4_API int nvfp4_selftest_wait_timeout(int32_t *flag, int kind, int64_t limit_ns,
                                           cudaStream_t stream);
+
+/* moe_nvfp4_gate_up (SiLU) and nvfp4_int8_matmul with loads that never come: in the kernel of
+ * few tokens the first CTA of each cluster leaves out its first weights, in that of many tokens
+ * one CTA of each pair the first loads of the pair's second tile.  Every wait is bounded by 2 ms
+ * instead of 2 s.  The kernel sets bit 1 of *error_flag, writes NaN for what it could not compute
+ * and returns.  error_flag must be given and T > 0 (else EINVAL); otherwise as those calls. */
+NVFP4_API int nvfp4_selftest_gate_up_timeout(const __nv_bfloat16 *x, const __nv_bfloat16 *w_gu,
+                                             int64_t T, int64_t H, int64_t I, __nv_bfloat16 *h,
+                                             __nv_bfloat16 *gu, int32_t *error_flag,
+                                             cudaStream_t stream);
+NVFP4_API int nvfp4_selftest_int8_matmul_timeout(const int8_t *a, const float *a_scales,
+                                                 const int8_t *w, const float *w_scales,
+                                                 int64_t T, int64_t N, int64_t K,
+                                                 __nv_bfloat16 *out, int32_t *error_flag,
+                                                 cudaStream_t stream);
 
 #ifdef __cplusplus
 }

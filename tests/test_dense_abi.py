@@ -148,3 +148,16 @@ def test_binding_checks_tensors(lib):
     for c in calls:
         with pytest.raises(ValueError):
             c()
+
+
+def test_the_timeout_hooks(lib):
+    gate = entry(lib, "nvfp4_selftest_gate_up_timeout", [P, P, I64, I64, I64, P, P, P],
+                 dict(x=OK, w=OK, T=4, H=64, I=32, h=OK, gu=None, flag=OK))
+    prod = entry(lib, "nvfp4_selftest_int8_matmul_timeout", [P, P, P, P, I64, I64, I64, P, P],
+                 dict(a=OK, sa=OK, w=OK, sw=OK, T=4, N=64, K=64, out=OK, flag=OK))
+    for call in (gate, prod):
+        for bad in (dict(flag=None), dict(flag=OK + 2), dict(T=0), dict(T=-1), dict(w=None)):
+            assert call(**bad) == -1, bad
+        assert call(T=1 << 30) == -2
+    assert gate(x=OK + 2) == -1 and gate(I=12) == -2
+    assert prod(out=OK + 8) == -1 and prod(K=72) == -2
