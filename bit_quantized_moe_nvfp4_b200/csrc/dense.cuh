@@ -51,7 +51,8 @@ struct DenseArgs {
   // rows.  split kernel: D rows are the output's columns, unless ROWS.
   int64_t M, N, K;
   int64_t half;                // kEpiGate: I, the rows of the gate half of w_gu
-  const float *m_scale;        // kEpiScale: scale of each D row
+  const float *m_scale;        // kEpiScale: scale of each D row (ordinary loads: the kernel before
+                               //            may write them while this one is already resident)
   const float *n_scale;        //            scale of each D column
   __nv_bfloat16 *out;          // split kernel: output, `ld` elements a row
   __nv_bfloat16 *gu;           // split kernel, kEpiGate: [cols, 2 half] pre-activations, or null
@@ -349,7 +350,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
         }
       } else {
         const int row = row0 + lane;
-        const float ms = (EPI == kEpiScale && row < p.M) ? __ldg(p.m_scale + row) : 0.f;
+        const float ms = (EPI == kEpiScale && row < p.M) ? p.m_scale[row] : 0.f;
         for (int c = 0; c < it.width / 64; ++c) {
           const int x = it.nt * 256 + it.part * it.width + c * 64;
           uint32_t o[32];
@@ -362,7 +363,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
               float f[4];
               if (EPI == kEpiScale) {
                 const int col = x + hf * 32 + k * 4;
-                const float4 ns = col < p.N ? __ldg(reinterpret_cast<const float4 *>(p.n_scale + col))
+                const float4 ns = col < p.N ? *reinterpret_cast<const float4 *>(p.n_scale + col)
                                             : make_float4(0.f, 0.f, 0.f, 0.f);
                 f[0] = (float)(int)v[4 * k] * ms * ns.x;
                 f[1] = (float)(int)v[4 * k + 1] * ms * ns.y;
@@ -644,8 +645,8 @@ __global__ void __launch_bounds__(kSThreads, 2)
         v.x = gate_act<ACT>(v.x) * u.x, v.y = gate_act<ACT>(v.y) * u.y;
         v.z = gate_act<ACT>(v.z) * u.z, v.w = gate_act<ACT>(v.w) * u.w;
       } else if (EPI == kEpiScale) {
-        const float ts = __ldg(p.n_scale + row);
-        const float4 ms = __ldg(reinterpret_cast<const float4 *>(p.m_scale + m0 + m));
+        const float ts = p.n_scale[row];
+        const float4 ms = *reinterpret_cast<const float4 *>(p.m_scale + m0 + m);
         v.x = v.x * ts * ms.x, v.y = v.y * ts * ms.y;
         v.z = v.z * ts * ms.z, v.w = v.w * ts * ms.w;
       }

@@ -49,8 +49,8 @@ __global__ void __launch_bounds__(256) gate_grad_kernel(const __nv_bfloat16 *gu,
     const int64_t t = e / nv;
     const int c = (int)(e - t * nv);
     const uint4 *row = reinterpret_cast<const uint4 *>(gu + t * 2 * I);
-    const uint4 gv = ldg_stream(row + c), uv = ldg_stream(row + nv + c);
-    const uint4 dv = ldg_stream(reinterpret_cast<const uint4 *>(dh) + e);
+    const uint4 gv = ld_stream(row + c), uv = ld_stream(row + nv + c);
+    const uint4 dv = ld_stream(reinterpret_cast<const uint4 *>(dh) + e);
     const uint32_t g[4] = {gv.x, gv.y, gv.z, gv.w}, u[4] = {uv.x, uv.y, uv.z, uv.w};
     const uint32_t d[4] = {dv.x, dv.y, dv.z, dv.w};
     uint32_t og[4], ou[4];

@@ -80,10 +80,8 @@ __device__ __forceinline__ uint4 pack8(const float2 (&f)[4]) {
   return make_uint4(pack_bf16x2(f[0].x, f[0].y), pack_bf16x2(f[1].x, f[1].y),
                     pack_bf16x2(f[2].x, f[2].y), pack_bf16x2(f[3].x, f[3].y));
 }
-__device__ __forceinline__ uint4 ldg8(const __nv_bfloat16 *p, int c) {
-  return __ldg(reinterpret_cast<const uint4 *>(p) + c);
-}
-// An ordinary load, which stores that follow it may overwrite.
+// Weights and gates too are read by ordinary loads: the kernel before may write them while this
+// one is already resident, and of one row an output may be the gate's tensor.
 __device__ __forceinline__ uint4 ld8(const __nv_bfloat16 *p, int c) {
   return reinterpret_cast<const uint4 *>(p)[c];
 }
@@ -313,7 +311,7 @@ __global__ void __launch_bounds__(max_threads<MAXT>(), row_ctas(MAXT))
         const int c = me + i * tpr;
         float2 y[4], w[4];
         unpack8(feed.get(at, 0, i), y);
-        unpack8(ldg8(p.w, c), w);
+        unpack8(ld8(p.w, c), w);
 #pragma unroll
         for (int j = 0; j < 4; ++j) y[j] = mul2(mul2(y[j], both(r)), w[j]);
         stg8(out, c, y);
@@ -328,7 +326,7 @@ __global__ void __launch_bounds__(max_threads<MAXT>(), row_ctas(MAXT))
           if (!feed.in(i)) continue;
           float2 w[4];
           unpack8(feed.get(at, 0, i), y[i]);
-          unpack8(ldg8(p.w, me + i * tpr), w);
+          unpack8(ld8(p.w, me + i * tpr), w);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             y[i][j] = mul2(mul2(y[i][j], both(r)), w[j]);
@@ -375,7 +373,7 @@ __global__ void __launch_bounds__(max_threads<MAXT>(), row_ctas(MAXT))
         float2 w[4], q[4];
         unpack8(feed.get(at, 0, i), o[i]);
         unpack8(feed.get(at, 1, i), q);
-        unpack8(ldg8(p.w, c), w);
+        unpack8(ld8(p.w, c), w);
         if (p.gh) {   // a gate for each value is a third row array
           float2 g[4];
           unpack8(p.gt ? feed.get(at, 2, i) : ld8(p.gate, c), g);
@@ -399,7 +397,7 @@ __global__ void __launch_bounds__(max_threads<MAXT>(), row_ctas(MAXT))
           if (!feed.in(i)) continue;
           const int c = me + i * tpr;
           float2 w[4];
-          unpack8(ldg8(p.w_next, c), w);
+          unpack8(ld8(p.w_next, c), w);
 #pragma unroll
           for (int j = 0; j < 4; ++j) w[j] = mul2(w[j], mul2(o[i][j], both(r2)));
           stg8(out, c, w);
@@ -472,7 +470,7 @@ __global__ void __launch_bounds__(max_threads<MAXT>(), grad_row_ctas(MAXT, VPT, 
       float2 x[4], d[4], w[4];
       unpack8(feed.get(at, 0, i), x);
       unpack8(feed.get(at, 1, i), d);
-      unpack8(ldg8(p.w, c), w);
+      unpack8(ld8(p.w, c), w);
       if (GATE >= kChannelGate) {
         float2 g[4];
         unpack8(GATE == kFullGate ? feed.get(at, 2, i) : ld8(p.gate, c), g);
@@ -506,7 +504,7 @@ __global__ void __launch_bounds__(max_threads<MAXT>(), grad_row_ctas(MAXT, VPT, 
       float2 x[4], d[4], w[4], o[4];
       unpack8(feed.get(at, 0, i), x);   // read again: registers hold the column sums
       unpack8(feed.get(at, 1, i), d);
-      unpack8(ldg8(p.w, c), w);
+      unpack8(ld8(p.w, c), w);
       float2 g[4];   // before the stores: of one row, any output may be the gate's tensor
       if (GATE >= kChannelGate)
         unpack8(GATE == kFullGate ? feed.get(at, 2, i) : ld8(p.gate, c), g);
@@ -629,7 +627,7 @@ __global__ void __launch_bounds__(1024) norm_grad_sum_kernel(const float *part_w
   if (c < H) {
 #pragma unroll 8
     for (int i = q; i < P; i += 128) {
-      const float4 x = __ldg(reinterpret_cast<const float4 *>(part + (int64_t)i * H + c));
+      const float4 x = *reinterpret_cast<const float4 *>(part + (int64_t)i * H + c);
       v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
     }
   }

@@ -271,3 +271,119 @@ def test_calls_from_another_current_device(nv, monkeypatch):
         assert next(looks, None) is None   # looked twice: refused, then taken
         for p, q in zip(*(t if isinstance(t, tuple) else (t,) for t in (got, want))):
             assert torch.equal(p, q)
+
+
+def test_scales_written_by_the_kernel_before(nv):
+    """Token after token through the same buffers: the product takes the codes and the scale
+    that the launch before it has just written, not those of the token before."""
+    N, K, n = 4096, 1024, 24
+    _, _, w, sw = (t.cuda() for t in case(1, N, K))
+    g = torch.Generator().manual_seed(2)
+    xs = [(torch.randn(1, K, generator=g) * 2.0 ** (k % 7)).bfloat16().cuda() for k in range(n)]
+    want = []
+    for x in xs:
+        q, s = nv.nvfp4_int8_quantize(x)
+        torch.cuda.synchronize()
+        want.append(nv.nvfp4_int8_matmul(q, s, w, sw))
+        torch.cuda.synchronize()
+    q = torch.empty(1, K, dtype=torch.int8, device="cuda")
+    s = torch.empty(1, device="cuda")
+    outs = [torch.empty(1, N, dtype=torch.bfloat16, device="cuda") for _ in range(n)]
+
+    def chain():
+        for x, o in zip(xs, outs):
+            nv.nvfp4_int8_quantize(x, codes=q, scales=s)
+            nv.nvfp4_int8_matmul(q, s, w, sw, out=o)
+
+    chain()
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, v) for o, v in zip(outs, want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        chain()
+    for _ in range(50):
+        for o in outs:
+            o.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, v) for o, v in zip(outs, want))
+
+
+FIRST_CALLS_IN_A_CAPTURE = """
+import torch
+import bit_quantized_moe_nvfp4_b200 as nv
+g = torch.Generator().manual_seed(1)
+r = lambda *s: torch.randn(s, generator=g).bfloat16().cuda()
+def data(T):
+    return r(T, 512), r(512), r(1, 512), r(2 * 640, 512) * 0.05, r(T, 640)
+def run(x, w, gate, wg, dh):
+    y = nv.moe_nvfp4_pre_norm(x, w, 1e-5)
+    gu = torch.empty(len(x), 1280, dtype=torch.bfloat16, device="cuda")
+    h = nv.moe_nvfp4_gate_up(y, wg, gu=gu)
+    q, s = nv.nvfp4_int8_quantize(h)
+    z = nv.nvfp4_int8_matmul(q, s, q[:8].contiguous(), s[:8].contiguous())
+    dx, dw = nv.moe_nvfp4_gate_up_backward(dh, y, wg, gu)
+    out = nv.moe_nvfp4_post_norm(dx, w, x, 1e-5, gate=gate, next_weight=w)
+    return (h, z, dx, dw) + out + nv.moe_nvfp4_post_norm_backward(x, dx, w, 1e-5, gate=gate)
+sets = [data(T) for T in (9, 1700)]
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = [run(*d) for d in sets]
+graph.replay()
+torch.cuda.synchronize()
+for o, d in zip(got, sets):
+    assert all(torch.equal(p, q) for p, q in zip(o, run(*d)))
+print("same")
+"""
+
+
+def test_first_calls_of_a_process_inside_a_capture():
+    """What a launch looks up once (maps, limits, residency) may be looked up in a capture."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS_IN_A_CAPTURE], cwd=root, timeout=300,
+                       capture_output=True, text=True)
+    assert r.returncode == 0 and r.stdout.endswith("same\n"), r.stderr[-2000:]
+
+
+def test_calls_from_several_host_threads(nv):
+    """Four threads, each on its own stream, sizes in another order: every result is the one that
+    a call alone gives."""
+    import threading
+    H, I = 512, 768
+    g = torch.Generator().manual_seed(5)
+    r = lambda *s: torch.randn(s, generator=g).bfloat16().cuda()
+    w, wg = r(H), r(2 * I, H) * 0.05
+    wq, ws = nv.nvfp4_int8_quantize(r(1032, I))
+
+    def step(x):
+        h = nv.moe_nvfp4_gate_up(nv.moe_nvfp4_pre_norm(x, w, EPS), wg)
+        return (h, nv.nvfp4_int8_matmul(*nv.nvfp4_int8_quantize(h), wq, ws)) + \
+            nv.moe_nvfp4_pre_norm_backward(x, x, w, EPS)
+
+    xs = [r(T, H) for T in (1, 30, 200, 1100)]
+    want = [step(x) for x in xs]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def worker(k):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for n in range(12):
+                    i = (n + k) % len(xs)
+                    got = step(xs[i])
+                    torch.cuda.current_stream().synchronize()
+                    if not all(torch.equal(p, q) for p, q in zip(got, want[i])):
+                        wrong.append((k, n))
+        except Exception as e:   # a thread's failure has to reach the test
+            wrong.append((k, repr(e)))
+
+    threads = [threading.Thread(target=worker, args=(k,)) for k in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong

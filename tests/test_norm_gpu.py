@@ -402,3 +402,37 @@ def test_smallest_eps(nv, no_nan, H):
     # the other rows: eps is nothing beside mean(x^2)
     rx, rm, *_ = grads(x[[0, 2, 3]], w, None, d[[0, 2, 3]], 1.0)
     close(dx[[0, 2, 3]], rx, 2 * (E + EPS) * rm)
+
+
+def test_a_gate_written_by_the_kernel_before(nv):
+    """One row after another: a product writes the gate that the norm right behind it reads, into
+    the memory that the norm before read its gate from."""
+    H, n = 1024, 24
+    y, res, w = draw(1, 1, H).cuda(), draw(2, 1, H).cuda(), draw(3, H, std=0.1, mean=1.0).cuda()
+    src = [draw(10 + k, 1, H).cuda() for k in range(n)]
+    gates = [nv.moe_nvfp4_pre_norm(s, w, EPS) for s in src]
+    torch.cuda.synchronize()
+    want = []
+    for g in gates:
+        want.append(nv.moe_nvfp4_post_norm(y, w, res, EPS, gate=g))
+        torch.cuda.synchronize()
+    gate = torch.empty(1, H, dtype=torch.bfloat16, device="cuda")
+    outs = [torch.empty_like(y) for _ in range(n)]
+
+    def chain():
+        for s, o in zip(src, outs):
+            nv.moe_nvfp4_pre_norm(s, w, EPS, out=gate)
+            nv.moe_nvfp4_post_norm(y, w, res, EPS, gate=gate, out=o)
+
+    chain()
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, v) for o, v in zip(outs, want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        chain()
+    for _ in range(20):
+        for o in outs:
+            o.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, v) for o, v in zip(outs, want))
