@@ -1,8 +1,10 @@
 // occupancy.cu -- per-device launch facts shared by the kernel launchers: the SM count and
 // how many blocks of a kernel fit on one SM, each looked up once and cached.
 #include <atomic>
+#include <map>
 #include <mutex>
-#include <vector>
+#include <tuple>
+#include <utility>
 
 #include "moe.cuh"
 
@@ -24,90 +26,73 @@ int num_sms() {
   return n;
 }
 
+namespace {
+
+// What a launch is asked about: a kernel on a device with this block size, shared memory and
+// cluster size (0: no cluster).  Each answer is kept; how many there are is bounded by the kernels
+// and the block and memory sizes that they are launched with (the norms: up to 32 widths of block
+// and two memory sizes a kernel), not by the calls.
+using Key = std::tuple<const void *, int, int, size_t, int>;
+std::mutex g_mu;
+std::map<Key, int> g_answers;
+std::map<std::pair<const void *, int>, size_t> g_limits;
+
+template <typename Query>
+int answer(const Key &key, Query query) {   // with g_mu held
+  const auto it = g_answers.find(key);
+  if (it != g_answers.end()) return it->second;
+  int n = 0;
+  const cudaError_t e = query(&n);
+  if (e != cudaSuccess) {
+    set_last_cuda_error(e);
+    return -1;
+  }
+  g_answers[key] = n;
+  return n;
+}
+
+}  // namespace
+
 // Blocks of kernel k that fit on one SM at once with this block size and shared memory,
 // after raising the kernel's dynamic shared-memory limit to at least `smem`.  The limit is a
 // per-kernel, per-device attribute that only ever grows here (a call with less memory must
-// not lower it under a size another call still launches with), and the occupancy answer is
-// cached per kernel, device, block size and memory, so a steady stream of calls pays for
-// neither query again.
+// not lower it under a size another call still launches with).
 int resident_blocks_fn(const void *fn, int threads, size_t smem) {
-  struct Limit {
-    const void *fn;
-    int dev;
-    size_t smem;
-  };
-  struct Entry {
-    const void *fn;
-    int dev, threads;
-    size_t smem;
-    int nb;
-  };
-  static std::mutex mu;
-  static std::vector<Limit> limits;
-  static std::vector<Entry> cache;
   int dev = 0;
   cudaGetDevice(&dev);
-  std::lock_guard<std::mutex> lock(mu);
-  Limit *lim = nullptr;
-  for (Limit &l : limits)
-    if (l.fn == fn && l.dev == dev) lim = &l;
-  if (!lim || lim->smem < smem) {
+  std::lock_guard<std::mutex> lock(g_mu);
+  const auto lim = g_limits.find({fn, dev});
+  if (lim == g_limits.end() || lim->second < smem) {
     cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) {
       set_last_cuda_error(e);
       return -1;
     }
-    if (lim)
-      lim->smem = smem;
-    else
-      limits.push_back({fn, dev, smem});
+    g_limits[{fn, dev}] = smem;
   }
-  for (const Entry &c : cache)
-    if (c.fn == fn && c.dev == dev && c.threads == threads && c.smem == smem) return c.nb;
-  int nb = 0;
-  cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&nb, fn, threads, smem);
-  if (e != cudaSuccess) {
-    set_last_cuda_error(e);
-    return -1;
-  }
-  if (cache.size() < 256) cache.push_back({fn, dev, threads, smem, nb});
-  return nb;
+  return answer({fn, dev, threads, smem, 0}, [&](int *n) {
+    return cudaOccupancyMaxActiveBlocksPerMultiprocessor(n, fn, threads, smem);
+  });
 }
 
 int resident_clusters_fn(const void *fn, int threads, size_t smem, int size) {
-  struct Entry {
-    const void *fn;
-    int dev, threads, size;
-    size_t smem;
-    int n;
-  };
-  static std::mutex mu;
-  static std::vector<Entry> cache;
   int dev = 0;
   cudaGetDevice(&dev);
-  std::lock_guard<std::mutex> lock(mu);
-  for (const Entry &c : cache)
-    if (c.fn == fn && c.dev == dev && c.threads == threads && c.size == size && c.smem == smem)
-      return c.n;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)size);
-  cfg.blockDim = dim3((unsigned)threads);
-  cfg.dynamicSmemBytes = smem;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)size;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  int n = 0;
-  const cudaError_t e = cudaOccupancyMaxActiveClusters(&n, fn, &cfg);
-  if (e != cudaSuccess) {
-    set_last_cuda_error(e);
-    return -1;
-  }
-  if (cache.size() < 1024) cache.push_back({fn, dev, threads, size, smem, n});
-  return n;
+  std::lock_guard<std::mutex> lock(g_mu);
+  return answer({fn, dev, threads, smem, size}, [&](int *n) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)size);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)size;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaOccupancyMaxActiveClusters(n, fn, &cfg);
+  });
 }
 
 }  // namespace nvfp4
