@@ -436,3 +436,33 @@ def test_a_gate_written_by_the_kernel_before(nv):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(o, v) for o, v in zip(outs, want))
+
+
+# every (threads, vectors a thread) that row_shape gives, with few and with many rows: warp rows of
+# 1 to 6 vectors, CTAs of up to 256 threads with 1 to 4, of up to 1024 threads with 1 to 4
+LAYOUTS = [(5, 256), (5, 392), (5, 648), (9, 1000), (9, 1272), (9, 1536), (9, 1544), (300, 1544),
+           (300, 2048), (200, 4096), (300, 6144), (160, 6152), (300, 8192), (9, 8200), (160, 8200),
+           (160, 16384), (5, 16392), (160, 24576), (5, 24584)]
+
+
+@pytest.mark.parametrize("gate", ["none", "1", "t", "h", "th"])
+@pytest.mark.parametrize("T,H", LAYOUTS + SHAPES)
+def test_post_norm_of_every_layout(nv, no_nan, T, H, gate):
+    """T at least the SM count: rows of at most 8192 values take CTAs of 256 threads; fewer rows,
+    or longer ones: of 1024."""
+    test_post_norm(nv, T, H, gate)
+
+
+@pytest.mark.parametrize("gate", ["none", "1", "t", "h", "th"])
+@pytest.mark.parametrize("T,H", LAYOUTS + SHAPES)
+def test_post_norm_backward_of_every_layout(nv, no_nan, T, H, gate):
+    test_post_norm_backward(nv, T, H, gate)
+
+
+@pytest.mark.parametrize("T,H", LAYOUTS + SHAPES)
+def test_pre_norm_and_8_bit_rows_of_every_layout(nv, no_nan, T, H):
+    test_pre_norm(nv, T, H)
+    test_pre_norm_backward(nv, T, H, True)
+    if H % 16 == 0:
+        test_pre_norm_int8(nv, T, H)
+        test_int8_quantize_is_exact(nv, T, H)
