@@ -328,3 +328,11 @@ def test_huge_up_values_beside_a_closed_gate(nv):
     for act in (0, 1):
         _, dw = nv.moe_nvfp4_gate_up_backward(4 * dh, x, w, gu, act=act)
         assert (dw == 0).all()
+
+
+@pytest.mark.parametrize("T,H,I", [(3, 65536, 8), (300, 65536, 8), (3, 8, 65536), (300, 16, 65536)])
+def test_largest_widths(nv, T, H, I):
+    """H and I at their limits, in both kernels, forward and backward."""
+    test_gate_up(nv, T, H, I, 0)
+    test_gate_up_backward(nv, T, H, I, 0)
+    test_no_nan_comes_of_finite_inputs(nv, T, H, I, 0)

@@ -387,3 +387,19 @@ def test_calls_from_several_host_threads(nv):
     for t in threads:
         t.join()
     assert not wrong
+
+
+@pytest.mark.parametrize("T,K", [(3, 16), (130, 16), (130, 32768)])
+def test_largest_channels(nv, T, K):
+    """N at its limit (K at its limit: 32768 channels), the last channels among the rest."""
+    N = 1 << 24 if K == 16 else 1 << 15
+    g = torch.Generator(device="cuda").manual_seed(T)
+    a = torch.randint(-127, 128, (T, K), generator=g, dtype=torch.int8, device="cuda")
+    w = torch.randint(-127, 128, (N, K), generator=g, dtype=torch.int8, device="cuda")
+    sa = torch.rand(T, generator=g, device="cuda") + 0.1
+    sw = torch.rand(N, generator=g, device="cuda") + 0.1
+    out = nv.nvfp4_int8_matmul(a, sa, w, sw)
+    for n0 in (0, N // 2 - 64, N - 4096):
+        n1 = n0 + 4096
+        ref = (a.double() @ w[n0:n1].double().t()) * sa.double()[:, None] * sw[n0:n1].double()
+        assert ((out[:, n0:n1].double() - ref).abs() <= (B + 2.0 ** -22) * ref.abs()).all()

@@ -466,3 +466,20 @@ def test_pre_norm_and_8_bit_rows_of_every_layout(nv, no_nan, T, H):
     if H % 16 == 0:
         test_pre_norm_int8(nv, T, H)
         test_int8_quantize_is_exact(nv, T, H)
+
+
+@pytest.mark.parametrize("T,H", [(5, 264), (700, 1032), (300, 2056)])
+@pytest.mark.parametrize("gate", ["1", "t", "h", "th"])
+def test_gradients_in_the_place_of_weight_and_gate(nv, T, H, gate):
+    """dweight in weight's own tensor, dgate in gate's."""
+    y, d, w = draw(1, T, H).cuda(), draw(2, T, H, std=0.1).cuda(), draw(3, H).cuda()
+    g = gates(gate, T, H, 5).cuda()
+    want = nv.moe_nvfp4_post_norm_backward(d, y, w, EPS, gate=g, residual_scale=0.5)
+    a, b = w.clone(), g.clone()
+    got = nv.moe_nvfp4_post_norm_backward(d, y, a, EPS, gate=b, residual_scale=0.5, dweight=a,
+                                          dgate=b)
+    assert all(torch.equal(p, q) for p, q in zip(got, want))
+    want = nv.moe_nvfp4_pre_norm_backward(d, y, w, EPS)
+    a = w.clone()
+    got = nv.moe_nvfp4_pre_norm_backward(d, y, a, EPS, dweight=a)
+    assert all(torch.equal(p, q) for p, q in zip(got, want))
