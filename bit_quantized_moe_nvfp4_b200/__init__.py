@@ -572,6 +572,9 @@ def moe_nvfp4_forward_static(x, topk_ids, topk_w, w_gu, s_gu, g_gu, w_dn, s_dn, 
 
 
 # ------------------------------------------------------------------------------ dense operators
+# None of these calls is recorded by autograd, also where an input requires a gradient (as all
+# calls of this module): a training step calls the *_backward functions, for instance from a
+# torch.autograd.Function of its own.
 # One token's call is shorter on the GPU than in Python, so these helpers do little: the raw
 # stream handle instead of a Stream object (2 us less a call), one attribute test each.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",   # absent without CUDA
@@ -635,8 +638,8 @@ def _scratch(workspace, nbytes: int, like):
     """(workspace, its address, its bytes), allocated beside `like` when none is given."""
     if workspace is None:
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
-    elif workspace.dtype is not torch.uint8 or workspace.get_device() != like.get_device() \
-            or not workspace.is_contiguous():
+    elif not isinstance(workspace, torch.Tensor) or workspace.dtype is not torch.uint8 \
+            or workspace.get_device() != like.get_device() or not workspace.is_contiguous():
         raise ValueError("workspace: expected a contiguous torch.uint8 tensor on the inputs' "
                          "device")
     return workspace, workspace.data_ptr(), workspace.numel()
@@ -694,7 +697,8 @@ def moe_nvfp4_post_norm(y, weight, residual, eps: float, gate=None, residual_sca
                         next_weight=None, out=None, next_out=None):
     """out = residual_scale * residual + gate * norm(y), with the norm of moe_nvfp4_pre_norm;
     gate bf16 [1 or T, 1 or H] or None.  With next_weight [H] also the following block's
-    pre-norm of out.  Returns out bf16 [T, H], or (out, next)."""
+    pre-norm of out.  Returns out bf16 [T, H], or (out, next).  The gradient of next is that of
+    moe_nvfp4_pre_norm at out; it reaches moe_nvfp4_post_norm_backward through dout."""
     bf = torch.bfloat16
     T, H, dev, py = _matrix(y, bf, "y")
     if dev != _current_device():
@@ -785,7 +789,8 @@ def moe_nvfp4_gate_up(x, w_gu, act: int = ACT_SILU, h=None, gu=None,
                       error_flag=None) -> torch.Tensor:
     """h = act(x W_g^T) * (x W_u^T) in one kernel; x bf16 [T, H]; w_gu bf16 [2I, H], gate rows
     first.  gu bf16 [T, 2I], when given, receives the pre-activations that
-    moe_nvfp4_gate_up_backward takes.  Returns h bf16 [T, I]."""
+    moe_nvfp4_gate_up_backward takes.  error_flag int32 [1], when given, gets bit 1 if a wait on
+    the device gave up; what could then not be computed is NaN.  Returns h bf16 [T, I]."""
     bf = torch.bfloat16
     T, H, dev, px = _matrix(x, bf, "x")
     if dev != _current_device():
@@ -829,7 +834,8 @@ def moe_nvfp4_gate_up_backward(dh, x, w_gu, gu, act: int = ACT_SILU, dx=None, dw
 
 def nvfp4_int8_quantize(x, codes=None, scales=None):
     """Rows of x bf16 [rows, cols] -> (codes int8 [rows, cols], scales fp32 [rows]):
-    scale = max |x| / 127, code = the integer nearest to x / scale."""
+    scale = max |x| / 127, code = the integer nearest to x / scale.  A row with NaN or an infinity
+    gets the scale NaN."""
     T, K, dev, px = _matrix(x, torch.bfloat16, "x")
     if dev != _current_device():
         return _on(dev, nvfp4_int8_quantize, x, codes, scales)

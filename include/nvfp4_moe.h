@@ -402,7 +402,8 @@ NVFP4_API int moe_nvfp4_forward_w4a4_profiled(
  * before it is written, so an output may be the very tensor of an input of its type and shape
  * (the residual stream in place); no other overlap is allowed.  Infinite or NaN values stay in
  * their own row, except in the gradients that are summed over rows.  A row whose sum of squares
- * exceeds fp32 counts as infinitely long: its norm is 0.
+ * exceeds fp32 counts as infinitely long: its norm is 0 (and its gradients 0, or NaN where their
+ * own sums leave fp32 too).
  * Limits: H % 8 == 0, H <= 32768 (pre_norm_int8: H % 16 == 0).
  * Alignment: 16 bytes; a gate with gate_cols 1, and its gradient, 2 bytes; scales 4 bytes.
  * Errors: EINVAL, ESHAPE, EWORKSPACE (backward), ECUDA.
@@ -434,6 +435,7 @@ NVFP4_API int moe_nvfp4_post_norm(const __nv_bfloat16 *y, const __nv_bfloat16 *w
  *   post_norm:  as above with dout gate in the place of dy;  dresidual = residual_scale dout
  *               (NULL: not wanted);  dgate = dout weight n summed over the axes along which
  *               gate is broadcast, [gate_rows, gate_cols] (NULL exactly when gate is)
+ *   next:       dout + moe_nvfp4_pre_norm_backward's dx at out takes the place of dout
  * Sums over tokens are taken in an order that sizes and device fix: equal calls give equal
  * bits.  Workspace: moe_nvfp4_norm_backward_workspace_size bytes, 16-byte aligned,
  * no initialisation; calls that share one must not overlap in time. */
@@ -478,7 +480,8 @@ NVFP4_API int moe_nvfp4_gate_up(const __nv_bfloat16 *x, const __nv_bfloat16 *w_g
  *   dw_gu = bf16( [dg | du]^T x )       [2I, H], or NULL: not wanted (x may then be NULL)
  * with fp32 sums whose order sizes and device fix.  T == 0 sets dw_gu to zero.
  * Workspace: moe_nvfp4_gate_up_backward_workspace_size bytes, 16-byte aligned, no
- * initialisation.  Limits, alignment and error_flag as moe_nvfp4_gate_up.
+ * initialisation; calls that share one must not overlap in time.  Limits, alignment and
+ * error_flag as moe_nvfp4_gate_up.
  * Errors: EINVAL (also dx and dw_gu both NULL), ESHAPE, EWORKSPACE, ECUDA. */
 NVFP4_API size_t moe_nvfp4_gate_up_backward_workspace_size(int64_t T, int64_t I);
 NVFP4_API int moe_nvfp4_gate_up_backward(const __nv_bfloat16 *dh, const __nv_bfloat16 *x,
@@ -503,7 +506,8 @@ NVFP4_API int moe_nvfp4_gate_up_backward(const __nv_bfloat16 *dh, const __nv_bfl
 NVFP4_API int nvfp4_int8_quantize(const __nv_bfloat16 *x, int64_t rows, int64_t cols,
                                   int8_t *codes, float *scales, cudaStream_t stream);
 
-/* out[t, n] = bf16( (sum_k a[t, k] w[n, k]) a_scales[t] w_scales[n] ): exact int32 sums.
+/* out[t, n] = bf16( ((sum_k a[t, k] w[n, k]) a_scales[t]) w_scales[n] ): exact int32 sums, the
+ * two products in fp32 in this order.
  *   a [T, K] int8   a_scales [T] fp32   w [N, K] int8   w_scales [N] fp32   out [T, N] bf16
  * error_flag as in moe_nvfp4_gate_up.  No workspace.  T == 0 enqueues nothing.
  * Limits: K % 16 == 0, K <= 32768, N % 8 == 0, N <= 2^24, T < 2^30, T N <= 2^44.  Alignment:
