@@ -11,8 +11,10 @@
 //    tiles.  Every CTA holds 128 rows of A and 128 rows of B a stage, so the pair reads half
 //    the shared memory per flop that two single CTAs would.  Tiles are handed out in a fixed
 //    order; two TMEM accumulators let the epilogue of a tile run under the next one's MMAs.
-//    Bound by the tensor pipe and the power limit: 4096 x 4096 x 6144 bf16 with the gate 138 us
-//    (1,490 TFLOP/s, pipe 85% active at 1.53 GHz), 8-bit 4096 x 6144 x 6144 98 us (3,150).
+//    Bound by the tensor pipe and the power limit: 4096 x 4096 x 6144 bf16 with the gate 140 us
+//    (1,475 TFLOP/s, pipe 85% active), 8-bit 4096 x 6144 x 6144 96 us (3,220), both in a captured
+//    graph of a few milliseconds; 161 and 110 us in a loop of a second, where the power limit
+//    holds the clock at 1.36 and 1.44 GHz of 1.965.
 //  * dense_split_kernel, few tokens or small matrices: 128 x NT tiles of one CTA, the sum
 //    over K split over the CTAs of a cluster so that every SM streams its share of the
 //    weights.  Partial tiles meet in shared memory: each CTA adds its slice of the tile over

@@ -4,7 +4,9 @@
 //   dx = [dg | du] w_gu,  dw_gu = [dg | du]^T x              (two products)
 // The gradients' operands are used as they lie in memory (MN-major tensor-core operands).
 // dg and du are rounded to bf16, the type the tensor cores take; everything before and after
-// that is fp32 with one rounding.
+// that is fp32 with one rounding.  The second rounding costs dx and dw_gu 0.0023 of their 2-norm
+// against 0.0017 for the result's own alone; two bf16 terms for each of dg and du would save it at
+// twice the products' time.
 #include "dense.cuh"
 
 namespace nvfp4 {

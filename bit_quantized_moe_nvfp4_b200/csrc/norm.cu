@@ -10,14 +10,21 @@
 // With x in registers, mean(dn n) = r sum(dn x) / H, so both sums of a row come from one
 // pass over it and are reduced together.
 //
-// Every kernel here is bound by HBM: a row is read once and each output written once.  A row
-// of at most 1536 values belongs to a warp (no barrier); a longer one to a CTA.  CTAs are
-// persistent.  Each thread copies the 16-byte vectors that it will itself need of its next
-// rows into shared memory (cp.async), a row ahead, so loads stay in flight through the
-// reductions and stores of the present row, without registers or barriers for it.
-// Measured: post_norm with next, 16384 x 6144 and a channel gate, 137 us (805 MB, 5.9 TB/s);
-// gradients with a token gate, 4096 x 6144, 38 us (201 MB) and 6 us for the column sums;
-// quantize 4096 x 6144, 17 us (75 MB; issue slots 73% busy).
+// A row is read once and each output written once.  A row of at most 1536 values belongs to a
+// warp (no barrier); a longer one to a CTA.  CTAs are persistent.  Each thread copies the 16-byte
+// vectors that it will itself need of its rows into shared memory (cp.async).  Where two rows of
+// all arrays fit the CTA's share of shared memory that is done a row ahead, so loads stay in
+// flight through the reductions and stores of the present row, without registers or barriers for
+// it: with one or two arrays up to 24576 values a row.  With three (dskip, or a gate for each
+// value) only some widths have the room; neither 1032 nor 6144 does, and a row's loads start when
+// the row before has left its slots.
+// Long rows of one and two arrays are bound by HBM.  Captured in a graph: post_norm with next,
+// 16384 x 6144 and a channel gate, 137 us (805 MB, 5.9 TB/s); pre_norm 4096 x 6144, 17.7 us
+// (101 MB, 5.7 TB/s); gradients 4096 x 6144, with the 6 to 7 us of their column sums: no gate 41,
+// token gate 42 (201 MB, 4.8 TB/s), channel gate 50 (two CTAs an SM), full gate 56 (302 MB),
+// pre_norm's 36, with dskip 41.  The quantizer is near its issue limit (4096 x 6144, 15.5 us, 75
+// MB, issue slots 75% busy); short rows wait for memory (gradients with dskip of 8191 x 1032: 18
+// us for 68 MB, issue slots 46% busy, nothing in flight ahead).
 // All statistics and sums are fp32; each result is rounded once.  next is taken from the
 // unrounded out, and codes from the unrounded y.
 #include <algorithm>

@@ -41,7 +41,7 @@ def rms(x):
     return torch.rsqrt((x * x).mean(-1, keepdim=True) + EPS)
 
 
-# rows of a warp (H <= 1024), of a CTA of 256 threads, of 1024 threads; partly filled vectors
+# rows of a warp (H <= 1536), of a CTA of 256 threads, of 1024 threads; partly filled vectors
 SHAPES = [(1, 8), (3, 64), (5, 264), (9, 1024), (1, 1032), (7, 1536), (150, 2056), (2, 6144),
           (333, 6144), (160, 8200), (3, 32768)]
 
