@@ -483,3 +483,35 @@ def test_gradients_in_the_place_of_weight_and_gate(nv, T, H, gate):
     a = w.clone()
     got = nv.moe_nvfp4_pre_norm_backward(d, y, a, EPS, dweight=a)
     assert all(torch.equal(p, q) for p, q in zip(got, want))
+
+
+@pytest.mark.parametrize("T,H", [(3, 264), (200, 2056)])
+def test_gradients_through_next(nv, no_nan, T, H):
+    """The gradient of next reaches the block through dskip: pre_norm's at out, added to dout,
+    takes the place of dout.  out and that sum are rounded on the way (2^-8 of out moves n and r
+    by as much, 2^-8 of the sum itself): 4 2^-8 of the terms' magnitudes bound both."""
+    y, res, d, d2 = (draw(k, T, H) for k in range(4))
+    w, w2 = draw(5, H, std=0.1, mean=1.0), draw(6, H, std=0.1, mean=1.0)
+    c = lambda *ts: [t.cuda() for t in ts]
+    out, _ = nv.moe_nvfp4_post_norm(*c(y, w, res), EPS, residual_scale=0.75, next_weight=w2.cuda())
+    both, dw2 = nv.moe_nvfp4_pre_norm_backward(d2.cuda(), out, w2.cuda(), EPS, dskip=d.cuda())
+    dy, dw, _, dr = nv.moe_nvfp4_post_norm_backward(both, *c(y, w), EPS, residual_scale=0.75)
+    yd, wd, rd, vd = (t.double().requires_grad_() for t in (y, w, res, w2))
+    o = 0.75 * rd + wd * yd * rms(yd)
+    nxt = vd * o * rms(o)
+    want = torch.autograd.grad([o, nxt], [yd, wd, rd, vd], [d.double(), d2.double()])
+    # magnitudes: of d + r2 (dn + n |mean|) elementwise, through the norm's own gradient
+    with torch.no_grad():
+        _, m2, _, mw2, *_ = grads(o, w2, None, d2, 1.0)
+        total = d.double().abs() + m2
+        _, my, _, mw, *_ = grads(y, w, None, total, 1.0)
+    for got, ref, mag in zip((dy, dw, dr, dw2), want, (my, mw, 0.75 * total, mw2)):
+        close(got, ref, (4 * B + T * U) * mag)
+
+
+def test_workspaces_that_are_no_tensors(nv):
+    x, w = draw(1, 3, 64).cuda(), draw(2, 64).cuda()
+    for bad in ([0] * 64, "workspace", np.zeros(1 << 20, np.uint8), torch.zeros(1 << 20).cuda(),
+                torch.zeros(1 << 20, dtype=torch.uint8)):
+        with pytest.raises(ValueError):
+            nv.moe_nvfp4_pre_norm_backward(x, x, w, EPS, workspace=bad)
